@@ -29,7 +29,11 @@ EXPORTS = [
     "lens_op_attention_masked", "lens_sampler_default_options", "lens_shift_mu", "lens_time_grid",
     "lens_sample_euler_ex", "lens_dit_op_euler_cfg_rescaled", "lens_sampler_prepare", "lens_sampler_velocity",
     "lens_sampler_update", "lens_sampler_finish", "lens_op_quantize_w4", "lens_op_gemm_w4",
+    "lens_op_quantize_f8", "lens_op_gemm_f8", "lens_op_sandwich_norm", "lens_op_attention_window",
 ]
+
+# lens_dtype
+LENS_F32, LENS_BF16, LENS_F8E4M3 = 0, 1, 2
 
 KERNELS = {"none": 0, "attention": 1, "gemm_qkv": 2, "gemm_out": 3, "gemm_w13": 4, "gemm_w2": 5, "rmsnorm_mod": 6,
            "gemm_mod": 7}
@@ -114,6 +118,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lens_sampler_finish": (I, [P, P, P]),
         "lens_op_quantize_w4": (I, [P, L, L, P, P, P]),
         "lens_op_gemm_w4": (I, [P, P, P, P, P, I, I, I, P]),
+        "lens_op_quantize_f8": (I, [P, I, L, L, I, P, P, P]),
+        "lens_op_gemm_f8": (I, [P, P, P, P, P, P, I, I, I, I, P]),
+        "lens_op_sandwich_norm": (I, [P, P, I, I, I, I, P, P, P, P, P, L, F, F, P, P, I, P, P]),
+        "lens_op_attention_window": (I, [P, P, P, I, I, I, I, I, P, P, I, I, I, F, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -371,6 +379,37 @@ def lens_op_quantize_w4(w, rows: int, k: int, codes, scales, stream=None) -> Non
 def lens_op_gemm_w4(A, codes, scales, bias, C, M: int, N: int, K: int, stream=None) -> None:
     _check(load_library().lens_op_gemm_w4(_ptr(A), _ptr(codes), _ptr(scales), _ptr(bias), _ptr(C), M, N, K,
                                           _stream(stream)), "lens_op_gemm_w4")
+
+
+def lens_op_quantize_f8(x, x_type: int, rows: int, k: int, block_rows: int, codes, scales, stream=None) -> None:
+    _check(load_library().lens_op_quantize_f8(_ptr(x), x_type, rows, k, block_rows, _ptr(codes), _ptr(scales),
+                                              _stream(stream)), "lens_op_quantize_f8")
+
+
+def lens_op_gemm_f8(A, a_scales, W, w_scales, bias, C, c_type: int, M: int, N: int, K: int, stream=None) -> None:
+    _check(load_library().lens_op_gemm_f8(_ptr(A), _ptr(a_scales), _ptr(W), _ptr(w_scales), _ptr(bias), _ptr(C), c_type,
+                                          M, N, K, _stream(stream)), "lens_op_gemm_f8")
+
+
+def lens_op_sandwich_norm(h, y, y_type: int, M: int, D: int, rows_per_batch: int, post_gain, gate, pre_gain, shift,
+                          scale, mod_stride: int, residual_scale: float, eps: float, h_out, out, out_type: int,
+                          out_scales=None, stream=None) -> None:
+    _check(load_library().lens_op_sandwich_norm(_ptr(h), _ptr(y), y_type, M, D, rows_per_batch, _ptr(post_gain),
+                                                _ptr(gate), _ptr(pre_gain), _ptr(shift), _ptr(scale), mod_stride,
+                                                residual_scale, eps, _ptr(h_out), _ptr(out), out_type,
+                                                _ptr(out_scales), _stream(stream)), "lens_op_sandwich_norm")
+
+
+def lens_op_attention_window(q, k, v, B: int, heads: int, kv_heads: int, n_q: int, n_kv: int,
+                             q_start: Optional[Sequence[int]], kv_len: Optional[Sequence[int]], left: int, right: int,
+                             sinks: int, scale: float, out, stream=None) -> None:
+    """q_start and kv_len hold one entry per batch row; a list of another length is refused."""
+    qs, kl = _ints(q_start), _ints(kv_len)
+    if any(a is not None and a.size != B for a in (qs, kl)):
+        raise LensError(2, "lens_op_attention_window")
+    _check(load_library().lens_op_attention_window(_ptr(q), _ptr(k), _ptr(v), B, heads, kv_heads, n_q, n_kv, _iptr(qs),
+                                                   _iptr(kl), left, right, sinks, scale, _ptr(out),
+                                                   _stream(stream)), "lens_op_attention_window")
 
 
 def lens_op_euler_cfg(x, v_cond, v_uncond, n: int, dt: float, guidance: float, stream=None) -> None:

@@ -340,6 +340,85 @@ LENS_API lens_status lens_op_attention_masked(const uint16_t* q, const uint16_t*
                                               int n_txt, int n_img, const int* txt_len, uint16_t* out_txt,
                                               uint16_t* out_img, void* stream);
 
+/* Element types of the operations below that take more than one. */
+typedef enum lens_dtype {
+  LENS_F32 = 0,
+  LENS_BF16 = 1,
+  LENS_F8E4M3 = 2   /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448, no infinity */
+} lens_dtype;
+
+/* 8-bit operands with a scale per block of 128: for each block, scale =
+ * max(amax, 2^-116) / 448 in fp32 and code = e4m3(x * (448 / max(amax, 2^-116))),
+ * rounded to nearest even; code * scale stands for x.  A block that holds a NaN has
+ * scale NaN, one that holds an infinity scale inf, and both widen to NaN.
+ *   x          dev [rows, k], fp32 or bf16 (x_type), 16-byte aligned; k a multiple of 16
+ *   block_rows 1: a scale per row and 128 columns (activations); 128: a scale per
+ *              128 x 128 (weights).  The last blocks may be partial.
+ *   codes      dev uint8 [rows, k], 16-byte aligned
+ *   scales     dev fp32 [ceil(k / 128), ceil(rows / block_rows)]: block (r, g) at [g][r]
+ * Errors: INVALID_ARG (NULL, misaligned, x_type, block_rows), SHAPE (rows < 1 or > 2^30,
+ * k < 16, k % 16, k > 2^22). */
+LENS_API lens_status lens_op_quantize_f8(const void* x, lens_dtype x_type, int64_t rows, int64_t k, int block_rows,
+                                         uint8_t* codes, float* scales, void* stream);
+
+/* Matrix product of such operands: with a_scales [ceil(K/128), M] (block_rows 1) and
+ * w_scales [ceil(K/128), ceil(N/128)] (block_rows 128),
+ *   C[m, n] = sum_g a_scales[g][m] w_scales[g][n / 128] sum_{k in g} A[m, k] W[n, k] (+ bias[n])
+ * on the 8-bit tensor cores, each 128-wide block accumulated in fp32, scaled and added
+ * in fp32.
+ *   A dev e4m3 [M, K], W dev e4m3 [N, K], bias dev fp32 [N] or NULL,
+ *   C dev [M, N], fp32 or bf16 (c_type, rounded once).  A, W, C 16-byte aligned.
+ * Errors: INVALID_ARG (NULL, misaligned, c_type), SHAPE (M, N or K < 1, N or K not a
+ * multiple of 16, a size > 2^22). */
+LENS_API lens_status lens_op_gemm_f8(const uint8_t* A, const float* a_scales, const uint8_t* W, const float* w_scales,
+                                     const float* bias, void* C, lens_dtype c_type, int M, int N, int K, void* stream);
+
+/* The norms after one branch and before the next, with the gate and the residual scale
+ * between them, in one pass over the rows (b = row / rows_per_batch):
+ *   h_out = residual_scale * h + gate[b] * post_gain * y / rms(y)
+ *   out   = (1 + scale[b]) * pre_gain * h_out / rms(h_out) + shift[b]
+ * with rms(x) = sqrt(mean(x^2) + eps) over the D columns.
+ *   h          dev fp32 [M, D];  h_out dev fp32 [M, D], may be h itself
+ *   y          dev [M, D], fp32 or bf16 (y_type): the branch's output
+ *   post_gain, pre_gain  dev fp32 [D] or NULL (1)
+ *   gate       dev fp32 [D] per sample at b * mod_stride, or NULL (1)
+ *   shift, scale  dev fp32 [D] per sample at b * mod_stride, or NULL (0), each on its own
+ *   out        dev [M, D], bf16 or e4m3 (out_type); e4m3 is quantized as
+ *              lens_op_quantize_f8 with block_rows 1 does, from the fp32 value
+ *   out_scales dev fp32 [ceil(D / 128), M] for e4m3, ignored for bf16
+ * D a multiple of 16, 16 <= D <= 8192; mod_stride a multiple of 4; every pointer 16-byte
+ * aligned (out_scales 4).  h_out and h must be the same or not overlap.
+ * Errors: INVALID_ARG (NULL, misaligned, a type, eps <= 0, residual_scale not finite),
+ * SHAPE (M < 1, rows_per_batch < 1, D, mod_stride). */
+LENS_API lens_status lens_op_sandwich_norm(const float* h, const void* y, lens_dtype y_type, int M, int D,
+                                           int rows_per_batch, const float* post_gain, const float* gate,
+                                           const float* pre_gain, const float* shift, const float* scale,
+                                           int64_t mod_stride, float residual_scale, float eps, float* h_out,
+                                           void* out, lens_dtype out_type, float* out_scales, void* stream);
+
+/* Attention over a window of keys and the first tokens.  Query i of batch row b stands at
+ * position p = q_start[b] + i and attends key j when
+ *   j < kv_len[b]  and  j <= p + right  and  (j >= p - left  or  j < sinks):
+ * a window of `left` keys before and `right` keys after its own position, and the first
+ * `sinks` keys wherever the window is (right = 0 is causal, sinks included).  Over joint
+ * [text; image] tokens with sinks = n_txt every image token sees the whole text.
+ *   out = softmax(scale * q k^T) v over the attended keys, zeros where there are none.
+ *   q dev bf16 [B, heads, n_q, 64];  k, v dev bf16 [B, kv_heads, n_kv, 64], query head h
+ *   reads key head h / (heads / kv_heads);  out dev bf16 [B, n_q, heads * 64]
+ *   q_start  host int [B], >= 0, or NULL (0);  kv_len host int [B], 0..n_kv, or NULL (n_kv)
+ *   left, right  >= 0, or -1 for no bound on that side;  sinks >= 0
+ * Keys that a query does not attend have no effect on its output, whatever K and V hold
+ * there (a non-finite value inside the tile costs time).  n_q may be anything from one
+ * token against a long cache to all of them.  B <= 64; heads a multiple of kv_heads, at
+ * most 1024; q, k, v, out 16-byte aligned; out must not overlap q, k or v.
+ * Errors: INVALID_ARG (NULL, misaligned, scale not finite or <= 0, left or right < -1,
+ * sinks < 0), SHAPE (B, heads, kv_heads, n_q, n_kv < 1, lengths or starts out of range,
+ * q_start + n_q or n_kv > 2^30). */
+LENS_API lens_status lens_op_attention_window(const uint16_t* q, const uint16_t* k, const uint16_t* v, int B, int heads,
+                                              int kv_heads, int n_q, int n_kv, const int* q_start, const int* kv_len,
+                                              int left, int right, int sinks, float scale, uint16_t* out,
+                                              void* stream);
+
 /* Euler step with optional CFG on tokens: x -= dt * (vu + g (vc - vu)), or
  * x -= dt * vc when v_uncond is NULL.  x, v_cond, v_uncond dev fp32 [n]. */
 LENS_API lens_status lens_op_euler_cfg(float* x, const float* v_cond, const float* v_uncond, int64_t n,

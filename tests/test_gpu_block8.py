@@ -1,0 +1,93 @@
+"""The 8-bit and windowed operations run together, as the attention half of a block uses
+them: quantize the rows, project, attend a window with the text visible, project back,
+then both norms with the gate and the next branch's 8-bit operand."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import flow_matching_mmdit_b200 as L  # noqa: E402
+from tests.test_gpu_f8 import _widen  # noqa: E402
+from tests.test_gpu_window import mask_of  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    L.load_library()
+
+
+def rel(a, b):
+    return float((a.double() - b).norm() / b.norm())
+
+
+def test_attention_half_of_a_block():
+    B, n_txt, n_img, heads, D = 2, 40, 360, 4, 256
+    n, M = n_txt + n_img, 2 * 400
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+
+    def normal(*s, std=1.0):
+        return torch.randn(s, generator=g, device="cuda") * std
+
+    def quantized(x, block_rows, kind):
+        codes = torch.empty(x.shape, dtype=torch.uint8, device="cuda")
+        scales = torch.empty((-(-x.shape[1] // 128), -(-x.shape[0] // block_rows)), device="cuda")
+        L.lens_op_quantize_f8(x, kind, x.shape[0], x.shape[1], block_rows, codes, scales)
+        return codes, scales
+
+    x, h = normal(M, D).to(torch.bfloat16), normal(M, D)
+    wqkv, wo = quantized(normal(3 * D, D, std=0.1), 128, L.LENS_F32), quantized(normal(D, D, std=0.1), 128, L.LENS_F32)
+    bias = normal(3 * D)
+    gain, mod = 1 + normal(D, std=0.1), normal(B, 3, D, std=0.3)
+
+    # ---- the library, on one stream without a wait in between
+    xa = quantized(x, 1, L.LENS_BF16)
+    qkv = torch.empty((M, 3 * D), dtype=torch.bfloat16, device="cuda")
+    L.lens_op_gemm_f8(*xa, *wqkv, bias, qkv, L.LENS_BF16, M, 3 * D, D)
+    q, k, v = (t.contiguous() for t in qkv.view(B, n, 3, heads, 64).permute(2, 0, 3, 1, 4))
+    att = torch.empty((B, n, D), dtype=torch.bfloat16, device="cuda")
+    L.lens_op_attention_window(q, k, v, B, heads, heads, n, n, None, [n, n - 30], 50, 50, n_txt, 0.125, att)
+    aa = quantized(att.view(M, D), 1, L.LENS_BF16)
+    y = torch.empty((M, D), dtype=torch.bfloat16, device="cuda")
+    L.lens_op_gemm_f8(*aa, *wo, None, y, L.LENS_BF16, M, D, D)
+    h_out = torch.empty_like(h)
+    codes = torch.empty((M, D), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((D // 128, M), device="cuda")
+    L.lens_op_sandwich_norm(h, y, L.LENS_BF16, M, D, n, gain, mod[:, 0], None, mod[:, 1], mod[:, 2], 3 * D, 0.75, 1e-6,
+                            h_out, codes, L.LENS_F8E4M3, scales)
+    out = torch.empty((M, 3 * D), device="cuda")
+    L.lens_op_gemm_f8(codes, scales, *wqkv, bias, out, L.LENS_F32, M, 3 * D, D)
+    torch.cuda.synchronize()
+
+    # ---- the same steps in fp64, unrounded between them except for the 8-bit weights
+    W, Wo = _widen(*wqkv, 128), _widen(*wo, 128)
+    r = (x.double() @ W.t() + bias.double()).view(B, n, 3, heads, 64).permute(2, 0, 3, 1, 4)
+    o = torch.zeros((B, n, heads, 64), dtype=torch.float64, device="cuda")
+    for b in range(B):
+        m = mask_of(n, n, 0, [n, n - 30][b], 50, 50, n_txt)
+        for i in range(heads):
+            s = torch.where(m, r[0, b, i] @ r[1, b, i].t() * 0.125, -torch.inf)
+            o[b, :, i] = torch.softmax(s, 1) @ r[2, b, i]
+    yr = o.view(M, D) @ Wo.t()
+    of = torch.arange(M, device="cuda") // n
+    hr = 0.75 * h.double() + mod[of, 0].double() * gain.double() * yr / (yr.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    xr = (1 + mod[of, 2].double()) * hr / (hr.square().mean(1, keepdim=True) + 1e-6).sqrt() + mod[of, 1].double()
+    # e4m3 rounds a value by up to 2^-4 of it (0.026 rms over a 3-bit mantissa); the attention
+    # weights turn the error of the scores (rms of q.k / 8 is about 20 here: W has gain 1.6)
+    # into one of theirs, so the branch is held to its direction and the rest to rms bounds
+    cos = float((y.double() * yr).sum() / (y.double().norm() * yr.norm()))
+    assert cos > 0.7, cos
+    assert rel(qkv, (x.double() @ W.t() + bias.double())) < 0.04
+    step_y = att.view(M, D).double() @ Wo.t()
+    assert rel(y, step_y) < 0.04
+    yd = y.double()
+    hs = 0.75 * h.double() + mod[of, 0].double() * gain.double() * yd / (yd.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    assert rel(h_out, hs) < 1e-6
+    xs = (1 + mod[of, 2].double()) * hs / (hs.square().mean(1, keepdim=True) + 1e-6).sqrt() + mod[of, 1].double()
+    assert rel(_widen(codes, scales, 1), xs) < 0.04
+    assert rel(out, xs @ W.t() + bias.double()) < 0.04
+    assert rel(out, xr @ W.t() + bias.double()) < 0.5
+    assert np.isfinite(float(out.sum()))

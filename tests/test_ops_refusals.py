@@ -1,0 +1,77 @@
+"""Argument errors of the 8-bit and windowed operations: refused before any device call."""
+import ctypes
+import os
+
+import pytest
+
+from flow_matching_mmdit_b200 import binding
+
+P = ctypes.c_void_p
+BAD, SHAPE = 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(binding.LIB_PATH):
+        from flow_matching_mmdit_b200 import build
+        build.build()
+    return binding.load_library()
+
+
+def test_quantize_f8_refusals(lib):
+    def call(x=16, t=0, rows=4, k=128, br=1, codes=16, scales=16):
+        return lib.lens_op_quantize_f8(P(x), t, rows, k, br, P(codes), P(scales), None)
+    for kw in (dict(x=0), dict(codes=0), dict(scales=0), dict(t=2), dict(t=7), dict(br=2), dict(br=0), dict(x=8),
+               dict(codes=4), dict(scales=2)):
+        assert call(**kw) == BAD, kw
+    for kw in (dict(rows=0), dict(rows=-1), dict(rows=2 ** 30 + 1), dict(k=0), dict(k=24), dict(k=2 ** 22 + 16)):
+        assert call(**kw) == SHAPE, kw
+
+
+def test_gemm_f8_refusals(lib):
+    def call(a=16, sa=16, w=16, sw=16, bias=0, c=16, t=0, m=4, n=32, k=128):
+        return lib.lens_op_gemm_f8(P(a), P(sa), P(w), P(sw), P(bias), P(c), t, m, n, k, None)
+    for kw in (dict(a=0), dict(sa=0), dict(w=0), dict(sw=0), dict(c=0), dict(t=2), dict(a=8), dict(w=8), dict(c=8),
+               dict(sa=2), dict(sw=1), dict(bias=3)):
+        assert call(**kw) == BAD, kw
+    for kw in (dict(m=0), dict(n=0), dict(n=24), dict(k=0), dict(k=8), dict(k=136), dict(m=-3),
+               dict(n=2 ** 22 + 16), dict(m=2 ** 22 + 1), dict(k=2 ** 22 + 16)):
+        assert call(**kw) == SHAPE, kw
+
+
+def test_sandwich_norm_refusals(lib):
+    def call(h=16, y=16, yt=1, m=4, d=128, rpb=4, post=0, gate=0, pre=0, shift=0, scale=0, stride=128, a=1.0, eps=1e-6,
+             ho=16, out=16, ot=1, os_=0):
+        return lib.lens_op_sandwich_norm(P(h), P(y), yt, m, d, rpb, P(post), P(gate), P(pre), P(shift), P(scale), stride,
+                                         a, eps, P(ho), P(out), ot, P(os_), None)
+    nan, inf = float("nan"), float("inf")
+    for kw in (dict(h=0), dict(y=0), dict(ho=0), dict(out=0), dict(yt=2), dict(ot=0), dict(ot=2), dict(ot=2, os_=2),
+               dict(eps=0.0), dict(eps=nan), dict(eps=inf), dict(a=nan), dict(a=inf), dict(h=8), dict(y=4), dict(ho=24),
+               dict(out=8), dict(gate=4), dict(shift=8), dict(scale=8), dict(post=8), dict(pre=8)):
+        assert call(**kw) == BAD, kw
+    for kw in (dict(m=0), dict(d=0), dict(d=24), dict(d=8208), dict(rpb=0), dict(stride=-4), dict(stride=6)):
+        assert call(**kw) == SHAPE, kw
+
+
+def test_attention_window_refusals(lib):
+    def ints(v):
+        return (ctypes.c_int * len(v))(*v) if v is not None else None
+
+    def call(q=16, k=16, v=16, b=2, h=4, hk=2, nq=5, nkv=9, start=None, length=None, left=3, right=0, sinks=1,
+             scale=0.125, out=16):
+        return lib.lens_op_attention_window(P(q), P(k), P(v), b, h, hk, nq, nkv, ints(start), ints(length), left, right,
+                                            sinks, scale, P(out), None)
+    for kw in (dict(q=0), dict(k=0), dict(v=0), dict(out=0), dict(q=8), dict(k=8), dict(v=8), dict(out=8),
+               dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(left=-2),
+               dict(right=-2), dict(sinks=-1)):
+        assert call(**kw) == BAD, kw
+    for kw in (dict(b=0), dict(b=65), dict(h=0), dict(h=1025, hk=1025), dict(hk=0), dict(h=4, hk=3), dict(nq=0),
+               dict(nkv=0), dict(nkv=2 ** 30 + 1), dict(nq=2 ** 30 + 1), dict(start=[0, -1]),
+               dict(start=[2 ** 30, 0]), dict(length=[10, 1]), dict(length=[-1, 1])):
+        assert call(**kw) == SHAPE, kw
+
+
+def test_binding_refuses_lengths_for_another_batch():
+    with pytest.raises(binding.LensError) as ei:
+        binding.lens_op_attention_window(None, None, None, 2, 4, 4, 1, 8, [0], [8, 8], 1, 0, 0, 0.125, None, stream=0)
+    assert ei.value.status == SHAPE
