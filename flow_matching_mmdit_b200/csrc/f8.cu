@@ -1,7 +1,7 @@
-// 8-bit operands with a scale per block of 128, and the matrix product on them.
-#include <cuda_fp8.h>
-
+// 8-bit operands with a scale per block of 128: quantization, and the entry point of the
+// matrix product on them (f8_gemm.cu).
 #include "f8.cuh"
+#include "f8_gemm.h"
 #include "kernels.cuh"
 #include "lens_dit.h"
 
@@ -99,74 +99,6 @@ cudaError_t launch_quantize_f8(const void* x, bool bf16, int64_t rows, int64_t k
   return cudaGetLastError();
 }
 
-// ------------------------------------------------------------------ product
-// One 64 x 64 tile per CTA on the FMA pipe, both operands widened to fp32 in shared
-// memory 32 columns at a time; a thread holds 4 x 4 outputs.
-__device__ __forceinline__ void widen16(const uint8_t* src, float (&v)[16]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(src);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2_raw h =
-        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-    const float2 f = __half22float2(__half2(h));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-
-__global__ void __launch_bounds__(256) gemm_f8_simple_kernel(const uint8_t* __restrict__ A,
-                                                             const float* __restrict__ as,
-                                                             const uint8_t* __restrict__ W,
-                                                             const float* __restrict__ ws,
-                                                             const float* __restrict__ bias, void* __restrict__ C,
-                                                             bool bf16, int M, int N, int K) {
-  __shared__ float sa[64][33], sw[64][33];
-  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
-  const int tm = (threadIdx.x >> 4) * 4, tn = (threadIdx.x & 15) * 4;
-  const int nb = (N + kF8Group - 1) / kF8Group;
-  float acc[4][4] = {};
-  for (int g = 0; g * kF8Group < K; ++g) {
-    float part[4][4] = {};
-    for (int k0 = g * kF8Group; k0 < K && k0 < (g + 1) * kF8Group; k0 += 32) {
-      __syncthreads();
-      const int row = (threadIdx.x >> 1) & 63, c = 16 * (threadIdx.x & 1);
-      const bool is_a = threadIdx.x < 128;
-      const int r = (is_a ? m0 : n0) + row;
-      float v[16] = {};
-      if (r < (is_a ? M : N) && k0 + c < K) widen16((is_a ? A : W) + (int64_t)r * K + k0 + c, v);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) (is_a ? sa : sw)[row][c + i] = v[i];
-      __syncthreads();
-      for (int kk = 0; kk < 32; ++kk)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sa[tm + i][kk], sw[tn + j][kk], part[i][j]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (m0 + tm + i >= M) continue;
-      const float s = as[(int64_t)g * M + m0 + tm + i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n0 + tn + j < N) acc[i][j] = fmaf(s * ws[(int64_t)g * nb + (n0 + tn + j) / kF8Group], part[i][j], acc[i][j]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + tm + i, n = n0 + tn + j;
-      if (m >= M || n >= N) continue;
-      const float y = acc[i][j] + (bias ? bias[n] : 0.f);
-      if (bf16)
-        static_cast<__nv_bfloat16*>(C)[(int64_t)m * N + n] = __float2bfloat16_rn(y);
-      else
-        static_cast<float*>(C)[(int64_t)m * N + n] = y;
-    }
-}
-
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 constexpr int64_t kMaxRowsF8 = 1 << 30, kMaxSize = 1 << 22;
@@ -199,7 +131,8 @@ extern "C" lens_status lens_op_gemm_f8(const uint8_t* A, const float* a_scales, 
     return LENS_ERR_SHAPE;
   if (!aligned16(A) || !aligned16(W) || !aligned16(C) || !aligned4(a_scales) || !aligned4(w_scales) || !aligned4(bias))
     return LENS_ERR_INVALID_ARG;
-  gemm_f8_simple_kernel<<<dim3((M + 63) / 64, (N + 63) / 64), 256, 0, (cudaStream_t)stream>>>(
-      A, a_scales, W, w_scales, bias, C, c_type == LENS_BF16, M, N, K);
-  return cudaGetLastError() == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
+  int* err = op_err_ptr();
+  if (!err) return LENS_ERR_CUDA;
+  const F8Gemm g{A, W, a_scales, w_scales, bias, C, c_type == LENS_BF16, M, N, K};
+  return launch_gemm_f8(g, err, device_sms(), (cudaStream_t)stream) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
 }

@@ -1,0 +1,289 @@
+// Matrix product of 8-bit operands with a scale per block of 128 (lens_op_gemm_f8):
+//   C[m, n] = sum_g sa[g][m] sw[g][n / 128] P_g[m, n] (+ bias[n]),
+//   P_g[m, n] = sum_{k in block g} A[m, k] W[n, k].
+#include "f8_gemm.h"
+
+#include "f8.cuh"
+#include "gemm.h"
+#include "gemm_tc.cuh"
+#include "kernels.cuh"
+#include "smem_attr.h"
+
+namespace lens {
+
+namespace {
+
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// ------------------------------------------------------------------ tcgen05, CTA pairs
+// 256 x BN tiles by a cluster of two CTAs (cta_group::2, kind::f8f6f4), persistent.
+// The scales differ from one 128-wide k block to the next, so a tile's sum over k cannot
+// stay in the tensor cores' accumulator: each block's P_g goes to its own TMEM slot
+// (SLOTS of them in turn) and eight epilogue warps read it, scale it and add it to the
+// tile's sum in registers (BN / 2 a thread) while the tensor cores work on the next.
+//   warp 0      TMA: 128 rows of A and BN / 2 rows of W of each k block (128-byte rows)
+//   warp 1      MMA issuer (leader CTA): 4 x (M = 256, N = BN, K = 32) into a slot
+//   warps 2..9  scale and add, then the tile's output through shared memory by TMA
+//   full[s]    (leader)  TMA bytes of both CTAs
+//   empty[s]   (both)    the k block's MMAs are done: stage s may be refilled
+//   tfull[a]   (both)    slot a holds a k block's P_g
+//   tempty[a]  (leader)  both CTAs' epilogue warps have read slot a
+template <int BN>
+struct F8Cfg {
+  static constexpr int BK = 128;
+  static constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = (BN / 2) * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr uint32_t EPI_SLOT = 4096, EPI_BYTES = EPI_WARPS * EPI_SLOT;
+  static constexpr uint32_t BUDGET = 232448 - 1024 - 256 - EPI_BYTES;
+  static constexpr int STAGES = BUDGET / STAGE_BYTES > 8 ? 8 : BUDGET / STAGE_BYTES;
+  static constexpr int SLOTS = 512 / BN;
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_BYTES + 256;
+};
+
+struct F8GemmArgs {
+  int M, N, kblocks, tiles_m, total_tiles, nblocks;
+  const float *as, *ws, *bias;
+  int* err;
+};
+
+template <int BN, bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 1)
+    gemm_f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                        const __grid_constant__ CUtensorMap tmC, const F8GemmArgs a) {
+  using C = F8Cfg<BN>;
+  constexpr int STAGES = C::STAGES, SLOTS = C::SLOTS, COLS = BN / 2;   // columns a thread accumulates
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sW = smem + STAGES * C::A_BYTES;
+  uint8_t* sEpi = sW + STAGES * C::B_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + SLOTS;
+  uint64_t* drain = tempty + SLOTS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* peer_issued = tmem_slot + 1;
+  static_assert((2 * STAGES + 2 * SLOTS + 1) * 8 + 8 <= 256, "barriers overflow their reserve");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(&tfull[s], 1);
+      mbar_init(&tempty[s], 2 * C::EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *peer_issued = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_sync();      // set-up above touched only shared memory and TMEM
+
+  uint32_t prod_issued = 0;
+  bool prod_ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      for (int t = pair; t < a.total_tiles && prod_ok; t += npairs) {
+        const int m0 = (t % a.tiles_m) * 256 + 128 * (int)rank, n0 = (t / a.tiles_m) * BN + (BN / 2) * (int)rank;
+        for (int kb = 0; kb < a.kblocks; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, a.err)) {
+            prod_ok = false;
+            break;
+          }
+          if (rank == 0) mbar_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+          tma_load_2d_pair(sA + stage * C::A_BYTES, &tmA, &full[stage], kb * C::BK, m0);
+          tma_load_2d_pair(sW + stage * C::B_BYTES, &tmW, &full[stage], kb * C::BK, n0);
+          ++prod_issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // the leader reconciles both CTAs' loads if the pair aborts
+      if (rank == 1) st_shared_cluster_u32(mapa_shared(smem_u32(peer_issued), 0), prod_issued);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = umma_idesc_e4m3(256, BN);
+      uint32_t stage = 0, phase = 0, slot = 0, use = 0;
+      bool ok = true;
+      for (int t = pair; t < a.total_tiles && ok; t += npairs) {
+        for (int kb = 0; kb < a.kblocks; ++kb) {
+          if (!mbar_wait_sleep(&tempty[slot], use ^ 1, a.err) || !mbar_wait_sleep(&full[stage], phase, a.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = umma_desc_sw128(smem_u32(sA + stage * C::A_BYTES));
+          const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * C::B_BYTES));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + slot * BN, ad + 2 * k, wd + 2 * k, idesc, k > 0 ? 1u : 0u);
+          umma_commit_pair(&empty[stage], 0x3);
+          umma_commit_pair(&tfull[slot], 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+          if (++slot == SLOTS) {
+            slot = 0;
+            use ^= 1;
+          }
+        }
+      }
+      if (!ok) umma_drain_pair(drain);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
+    uint8_t* box = sEpi + (warp - 2) * C::EPI_SLOT;
+    const uint32_t leader_tempty = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t lane_addr = tmem + (uint32_t(quarter * 32) << 16) + part * COLS;
+    uint32_t slot = 0, use = 0, no_slot = 0;
+    bool ok = true;
+    for (int t = pair; t < a.total_tiles && ok; t += npairs) {
+      const int row0 = (t % a.tiles_m) * 256 + 128 * (int)rank + quarter * 32, row = row0 + lane;
+      const int n0 = (t / a.tiles_m) * BN + part * COLS;
+      const bool live = row < a.M;
+      const float* as = a.as + row;
+      // a column block past the last one holds no output: any block's scale will do
+      const float* ws = a.ws + min(n0 / kF8Group, a.nblocks - 1);
+      uint64_t acc[COLS / 2];
+#pragma unroll
+      for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
+      // scales of the next k block, loaded one block ahead
+      float s_next = live ? __ldg(as) * __ldg(ws) : 0.f;
+#pragma unroll 1
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        const float s = s_next;
+        if (live && kb + 1 < a.kblocks)
+          s_next = __ldg(as + (int64_t)(kb + 1) * a.M) * __ldg(ws + (int64_t)(kb + 1) * a.nblocks);
+        const uint64_t s2 = f2_pack(s, s);
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[slot], use, a.err))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < COLS / 32; ++c) {
+          float r[32];
+          tmem_ld32(lane_addr + slot * BN + 32 * c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[16 * c + i] = f2_fma(f2_pack(r[2 * i], r[2 * i + 1]), s2, acc[16 * c + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(leader_tempty + slot * 8);
+        if (++slot == SLOTS) {
+          slot = 0;
+          use ^= 1;
+        }
+      }
+      if (!ok) break;
+      constexpr int PER = BF16 ? 64 : 32;        // columns of one 128-byte box row
+#pragma unroll
+      for (int c = 0; c < COLS / PER; ++c) {
+        const int n = n0 + PER * c;
+        uint4 ch[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float v[PER / 8];
+#pragma unroll
+          for (int i = 0; i < PER / 16; ++i) f2_unpack(acc[(PER * c + PER / 8 * j) / 2 + i], v[2 * i], v[2 * i + 1]);
+          if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < PER / 8; ++i)
+              v[i] += n + PER / 8 * j + i < a.N ? __ldg(a.bias + n + PER / 8 * j + i) : 0.f;
+          }
+          if constexpr (BF16)
+            ch[j] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7]));
+          else
+            ch[j] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                               __float_as_uint(v[3]));
+        }
+        stage_and_ship<false, 1>(box, no_slot, ch, &tmC, n, row0, row0 < a.M && n < a.N);
+      }
+    }
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  cluster_sync_all();          // every role of both CTAs has left its loop
+  if (warp == 0 && lane == 0 && rank == 0 && (!prod_ok || err_raised(a.err)))
+    drain_pair_stages<STAGES>(full, [&](uint32_t) { return C::STAGE_BYTES; }, prod_issued, *peer_issued);
+  cluster_sync_all();          // no MMA, TMA or remote arrive of the pair is in flight
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int BN, bool BF16>
+cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
+  using C = F8Cfg<BN>;
+  CUtensorMap ta, tw, tc;
+  if (!encode_tmap_u8(&ta, g.A, g.M, g.K, 128) || !encode_tmap_u8(&tw, g.W, g.N, g.K, BN / 2) ||
+      !encode_tmap_out(&tc, g.C, BF16 ? 2 : 4, g.M, g.N, g.N))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> attr{0};
+  const cudaError_t e = ensure_smem_limit(gemm_f8_pair_kernel<BN, BF16>, (int)C::SMEM, attr);
+  if (e != cudaSuccess) return e;
+  F8GemmArgs a;
+  a.M = g.M;
+  a.N = g.N;
+  a.kblocks = (g.K + kF8Group - 1) / kF8Group;
+  a.nblocks = (g.N + kF8Group - 1) / kF8Group;
+  a.tiles_m = (g.M + 255) / 256;
+  a.total_tiles = a.tiles_m * ((g.N + BN - 1) / BN);
+  a.as = g.a_scales;
+  a.ws = g.w_scales;
+  a.bias = g.bias;
+  a.err = err;
+  const int pairs = a.total_tiles < sms / 2 ? a.total_tiles : sms / 2;
+  return launch_pdl(gemm_f8_pair_kernel<BN, BF16>, dim3(2 * pairs), dim3(C::THREADS), C::SMEM, st, ta, tw, tc, a);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_f8(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
+  const int64_t wide = ((g.M + 255) / 256) * (int64_t)((g.N + 255) / 256);
+  if (wide >= sms / 2) return g.bf16 ? launch_pair<256, true>(g, err, sms, st) : launch_pair<256, false>(g, err, sms, st);
+  return g.bf16 ? launch_pair<128, true>(g, err, sms, st) : launch_pair<128, false>(g, err, sms, st);
+}
+
+}  // namespace lens

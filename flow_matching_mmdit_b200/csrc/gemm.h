@@ -22,6 +22,10 @@ bool encode_tmap_out(CUtensorMap* m, const void* ptr, int elem_bytes, uint64_t r
 // box = d0 x box_rows x 1, 128-byte swizzle, zero fill out of bounds.
 bool encode_tmap_bf16_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box_rows);
 
+// 2D map over a row-major [rows, cols] matrix of bytes (cols a multiple of 16), box = 128
+// columns x box_rows rows, 128-byte swizzle, zero fill out of bounds.
+bool encode_tmap_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
+
 // 4-bit weights (int4 weight-only path, w4.cu).  A quantized [rows, k] matrix is
 //   codes  uint8 [rows, k / 2]: 32-bit word w of a row holds the codes of k in
 //          [8w, 8w + 8); the code of k = 8w + 2j sits in bits [4j, 4j + 4), that of

@@ -33,6 +33,11 @@ struct TextLengths {
   int n[kMaxRows];
 };
 
+// lens_dit.cu: the abort flag that the handle-free operations share on the current device
+// (nullptr when it cannot be had), and the current device's number of SMs
+int* op_err_ptr();
+int device_sms();
+
 // attention.cu (txt_len == nullptr: every text key is valid)
 cudaError_t launch_joint_attention(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v, int B,
                                    int heads, int n_txt, int n_img, __nv_bfloat16* out_txt, __nv_bfloat16* out_img,

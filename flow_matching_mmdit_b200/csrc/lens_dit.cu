@@ -189,7 +189,7 @@ struct KScope {
     LENS_CUDA(x);                   \
   } while (0)
 
-static int device_sms() {
+int lens::device_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
@@ -217,7 +217,7 @@ static GemmProblem base_problem(int M, int N, int K) {
 // ============================================================ module-level error flag
 // Used by the handle-free op entry points.
 __device__ int g_op_err;
-static int* op_err_ptr() {
+int* lens::op_err_ptr() {
   int* p = nullptr;
   if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_op_err) != cudaSuccess) return nullptr;
   return p;

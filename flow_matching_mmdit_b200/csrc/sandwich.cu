@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(1024) sandwich_norm_kernel(const SandwichArgs 
 #pragma unroll
     for (int j = 0; j < 8; ++j) s += y[j] * y[j];
   }
-  float r = rsqrtf(cta_sum(s, red[0]) / a.D + a.eps);
+  float r = __frsqrt_rn(cta_sum(s, red[0]) / a.D + a.eps);
   s = 0.f;
   if (on) {
     load8_or(a.gate, mod, 1.f, g);
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(1024) sandwich_norm_kernel(const SandwichArgs 
     o[0] = make_float4(h[0], h[1], h[2], h[3]);
     o[1] = make_float4(h[4], h[5], h[6], h[7]);
   }
-  r = rsqrtf(cta_sum(s, red[1]) / a.D + a.eps);
+  r = __frsqrt_rn(cta_sum(s, red[1]) / a.D + a.eps);
   if (on) {
     load8_or(a.scale, mod, 0.f, g);
     load8_or(a.pre_gain, col, 1.f, p);

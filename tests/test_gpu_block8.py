@@ -75,11 +75,12 @@ def test_attention_half_of_a_block():
     of = torch.arange(M, device="cuda") // n
     hr = 0.75 * h.double() + mod[of, 0].double() * gain.double() * yr / (yr.square().mean(1, keepdim=True) + 1e-6).sqrt()
     xr = (1 + mod[of, 2].double()) * hr / (hr.square().mean(1, keepdim=True) + 1e-6).sqrt() + mod[of, 1].double()
-    # e4m3 rounds a value by up to 2^-4 of it (0.026 rms over a 3-bit mantissa); the attention
-    # weights turn the error of the scores (rms of q.k / 8 is about 20 here: W has gain 1.6)
-    # into one of theirs, so the branch is held to its direction and the rest to rms bounds
+    # e4m3 rounds a value by up to 2^-4 of it, 0.026 rms over a 3-bit mantissa: each product
+    # of rounded rows is held to 0.04.  Scores here have a deviation of 3.4, so theirs are off
+    # by 0.026 * 3.4 * 2^(1/2) = 0.13, and so are the attention weights, whose errors average
+    # out over the keys: the whole chain is held to 0.2 (a cosine of 0.98)
     cos = float((y.double() * yr).sum() / (y.double().norm() * yr.norm()))
-    assert cos > 0.7, cos
+    assert cos > 0.98, cos
     assert rel(qkv, (x.double() @ W.t() + bias.double())) < 0.04
     step_y = att.view(M, D).double() @ Wo.t()
     assert rel(y, step_y) < 0.04
@@ -89,5 +90,5 @@ def test_attention_half_of_a_block():
     xs = (1 + mod[of, 2].double()) * hs / (hs.square().mean(1, keepdim=True) + 1e-6).sqrt() + mod[of, 1].double()
     assert rel(_widen(codes, scales, 1), xs) < 0.04
     assert rel(out, xs @ W.t() + bias.double()) < 0.04
-    assert rel(out, xr @ W.t() + bias.double()) < 0.5
+    assert rel(out, xr @ W.t() + bias.double()) < 0.2
     assert np.isfinite(float(out.sum()))
