@@ -3,6 +3,7 @@
 //   P_g[m, n] = sum_{k in block g} A[m, k] W[n, k].
 #include "f8_gemm.h"
 
+#include "f32x2.cuh"
 #include "f8.cuh"
 #include "gemm.h"
 #include "gemm_tc.cuh"
@@ -12,20 +13,6 @@
 namespace lens {
 
 namespace {
-
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
 
 // ------------------------------------------------------------------ tcgen05, CTA pairs
 // 256 x BN tiles by a cluster of two CTAs (cta_group::2, kind::f8f6f4), persistent.

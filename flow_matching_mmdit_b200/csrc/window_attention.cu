@@ -5,6 +5,8 @@
 // and hi = min(p + right + 1, kv_len[b]).
 #include <math.h>
 
+#include "f32x2.cuh"
+#include "gemm.h"
 #include "kernels.cuh"
 #include "lens_dit.h"
 #include "smem_attr.h"
@@ -13,9 +15,9 @@ namespace lens {
 
 namespace {
 
-// Bounds that are not given are replaced by one past the largest position, so that
-// p + right and p - left stay inside 32 bits.
-constexpr int kMaxPos = 1 << 30;
+// Largest number of keys and of positions; a window without a bound is this wide.  The sum
+// of a position (of a row past the last, too) and a width stays inside 32 bits.
+constexpr int kMaxPos = 1 << 29;
 
 struct WindowArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -92,11 +94,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
@@ -107,7 +104,6 @@ __global__ void __launch_bounds__(32 * kFewWarps) window_attention_few_kernel(co
                                                                               const RowSpans spans, int splits) {
   __shared__ float s_o[kFewWarps][16][66];    // partial O of each warp, then of the CTA in [0]
   __shared__ float s_m[kFewWarps][16], s_l[kFewWarps][16];
-  __shared__ float s_inv[16];
   __shared__ int s_redo[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int rank = blockIdx.x % splits, tile = blockIdx.x / splits, hk = blockIdx.y, b = blockIdx.z;
@@ -294,6 +290,401 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, cudaSt
   return cudaLaunchKernelEx(&cfg, window_attention_few_kernel, a, spans, splits);
 }
 
+// ------------------------------------------------------------------ many rows
+// One CTA per (256 query rows = two 128-row tiles X = 0, 1; head; batch row) on the tcgen05
+// tensor cores, with the roles of the joint-attention kernel (attention.cu): S_X = Q_X K^T
+// and O_X += P_X V accumulate in TMEM, P_X goes back to TMEM as the second product's A
+// operand, eight softmax warps a tile hold the running maximum and sum, and O_X is
+// rescaled only when a row's maximum grows by more than 2^8.
+//   warps 0..15 softmax (X = warp / 8);  16 TMA;  17 S issuer;  18 P V issuer
+// Key tiles of 128 that no row of the CTA attends are never read: the walk goes through
+// the tiles of the sinks and then those of the window.  A tile inside every row's range
+// takes no mask; in the others each score is compared with its row's range.
+// TMEM columns: S_0 [0,128), S_1 [128,256), O_0 [256,320), O_1 [320,384), P_0 [384,448),
+// P_1 [448,512).
+namespace tc {
+
+constexpr int BQ = 128, BKV = 128, STAGES = 3, THREADS = 608;
+constexpr uint32_t Q_BYTES = BQ * 64 * 2, KV_BYTES = BKV * 64 * 2;
+constexpr uint32_t OFF_KV = 2 * Q_BYTES, OFF_BAR = OFF_KV + STAGES * 2 * KV_BYTES;
+constexpr size_t SMEM = 1024 + OFF_BAR + 256;
+constexpr float kRescaleThreshold = 8.0f;          // log2 units
+
+struct Bars {
+  uint64_t q_full;
+  uint64_t kv_full[STAGES], kv_empty[STAGES];
+  uint64_t s_full[2];    // MMA -> softmax: S_X ready
+  uint64_t s_free[2];    // softmax -> MMA: S_X read into registers
+  uint64_t p_full[2];    // softmax -> MMA: P_X written, O_X rescaled
+  uint64_t pv_done[2];   // MMA -> softmax: O_X += P_X V finished
+  uint64_t stagger;      // tile 0 -> tile 1: tile 0 finished its first exponentials
+  uint64_t drain[2];     // each MMA issuer's own completion after an abort
+  uint32_t tmem_slot;
+};
+static_assert(sizeof(Bars) <= 256, "barriers overflow their shared-memory reserve");
+
+__global__ void __launch_bounds__(THREADS, 1)
+    window_attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WindowArgs a,
+                               const __grid_constant__ RowSpans spans, int* err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = sm;
+  uint8_t* sKV = sm + OFF_KV;
+  Bars& bar = *reinterpret_cast<Bars*>(sm + OFF_BAR);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.z, h = blockIdx.y, q0 = blockIdx.x * 2 * BQ;
+  const int start = spans.start[b], len = spans.len[b];
+  const int tiles = a.n_q - q0 > BQ ? 2 : 1;          // the second tile may hold no row
+  // key tiles: [0, sink_tiles), then first_tile, first_tile + 1, ... nkv of them in all
+  // that hold the keys any row of the CTA attends, [0, sink) and [lo, hi)
+  int nkv, sink_tiles, first_tile, sink, lo, hi;
+  {
+    const KeyRange first = key_range(a, start + q0, len);
+    const KeyRange last = key_range(a, start + min(q0 + 2 * BQ, a.n_q) - 1, len);
+    hi = last.hi;
+    lo = min(first.lo, hi);
+    sink = min(last.s, lo);
+    first_tile = lo / BKV;
+    const int window_tiles = hi > lo ? (hi + BKV - 1) / BKV - first_tile : 0;
+    sink_tiles = (sink + BKV - 1) / BKV;
+    if (window_tiles > 0) sink_tiles = min(sink_tiles, first_tile);
+    nkv = sink_tiles + window_tiles;
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bar.q_full, 1);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&bar.kv_full[s], 1);
+      mbar_init(&bar.kv_empty[s], 2);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bar.s_full[x], 1);
+      mbar_init(&bar.s_free[x], 8);
+      mbar_init(&bar.p_full[x], 8);
+      mbar_init(&bar.pv_done[x], 1);
+    }
+    mbar_init(&bar.stagger, 8);
+    mbar_init(&bar.drain[0], 1);
+    mbar_init(&bar.drain[1], 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 17) {
+    tmem_alloc(&bar.tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem_slot;
+  grid_dependency_sync();    // set-up above touched only shared memory and TMEM
+
+  if (warp == 16) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0 && nkv > 0) {
+      uint32_t last_parity[STAGES] = {0, 0, 0};
+      bool issued[STAGES] = {false, false, false};
+      bool ok = true;
+      const int bh = b * a.heads + h, bhk = b * a.kv_heads + h / (a.heads / a.kv_heads);
+      mbar_expect_tx(&bar.q_full, tiles * Q_BYTES);
+      for (int x = 0; x < tiles; ++x) tma_load_3d(sQ + x * Q_BYTES, &tmQ, &bar.q_full, 0, q0 + x * BQ, bh);
+      for (int j = 0; j < nkv; ++j) {
+        const int s = j % STAGES;
+        const uint32_t ph = (j / STAGES) & 1;
+        const int kt = j < sink_tiles ? j : first_tile + (j - sink_tiles);
+        if (!mbar_wait(&bar.kv_empty[s], ph ^ 1, err)) {
+          ok = false;
+          break;
+        }
+        mbar_expect_tx(&bar.kv_full[s], 2 * KV_BYTES);
+        tma_load_3d(sKV + s * 2 * KV_BYTES, &tmK, &bar.kv_full[s], 0, kt * BKV, bhk);
+        tma_load_3d(sKV + s * 2 * KV_BYTES + KV_BYTES, &tmV, &bar.kv_full[s], 0, kt * BKV, bhk);
+        issued[s] = true;
+        last_parity[s] = ph;
+      }
+      mbar_wait_drain(&bar.q_full, 0);
+      // after an abort the consumers may not have waited for every stage filled here
+      if (!ok || err_raised(err))
+        for (int s = 0; s < STAGES; ++s)
+          if (issued[s]) mbar_wait_drain(&bar.kv_full[s], last_parity[s]);
+    }
+    __syncwarp();
+  } else if (warp == 17) {
+    // ---------------------------------------------------------------- S issuer
+    if (lane == 0 && nkv > 0) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16(128, BKV);
+      bool ok = mbar_wait(&bar.q_full, 0, err);
+      tc_fence_after();
+      for (int j = 0; ok && j < nkv; ++j) {
+        const int s = j % STAGES;
+        ok = mbar_wait(&bar.kv_full[s], (j / STAGES) & 1, err);
+        if (!ok) break;
+        const uint64_t kdesc = umma_desc_sw128(smem_u32(sKV + s * 2 * KV_BYTES));
+        for (int x = 0; x < tiles; ++x) {
+          if (j > 0 && !mbar_wait(&bar.s_free[x], (j - 1) & 1, err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t qdesc = umma_desc_sw128(smem_u32(sQ + x * Q_BYTES));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(tmem + x * 128, qdesc + 2 * k, kdesc + 2 * k, idesc_s, k > 0 ? 1u : 0u);
+          umma_commit(&bar.s_full[x]);
+        }
+        if (!ok) break;
+        umma_commit(&bar.kv_empty[s]);
+      }
+      if (!ok) umma_drain(&bar.drain[0]);   // no S MMA still runs when TMEM is freed
+    }
+    __syncwarp();
+  } else if (warp == 18) {
+    // ---------------------------------------------------------------- P V issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_pv = umma_idesc_bf16_bmn(128, 64);
+      bool ok = true;
+      for (int j = 0; ok && j < nkv; ++j) {
+        const int s = j % STAGES;
+        const uint32_t vbase = smem_u32(sKV + s * 2 * KV_BYTES + KV_BYTES);
+        for (int x = 0; x < tiles; ++x) {
+          if (!mbar_wait(&bar.p_full[x], j & 1, err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t vdesc = umma_desc_sw128_mn(vbase + k * 2048);
+            umma_bf16_ts(tmem + 256 + x * 64, tmem + 384 + x * 64 + 8 * k, vdesc, idesc_pv,
+                         (j > 0 || k > 0) ? 1u : 0u);
+          }
+          umma_commit(&bar.pv_done[x]);
+        }
+        if (!ok) break;
+        umma_commit(&bar.kv_empty[s]);
+      }
+      if (!ok) umma_drain(&bar.drain[1]);   // no P V MMA still runs when TMEM is freed
+    }
+    __syncwarp();
+  } else if ((warp >> 3) < tiles) {
+    // ---------------------------------------------------------------- softmax
+    // Warp (quarter, half) of tile X reads TMEM lanes quarter*32 + half*16 + [0, 16); each
+    // thread holds rows rlo and rlo + 8, 32 of the 128 keys of each (columns 8g + cq +
+    // {0, 1}); the four threads of a row combine maxima by shuffles.
+    const int x = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int wrow = x * BQ + quarter * 32 + half * 16, rlo = wrow + (lane >> 2);
+    const uint32_t lane_addr = tmem + (uint32_t(quarter * 32 + half * 16) << 16);
+    const uint32_t s_col = x * 128, o_col = 256 + x * 64, p_col = 384 + x * 64;
+    const int cq = 2 * (lane & 3);
+    const KeyRange k0 = key_range(a, start + q0 + rlo, len), k1 = key_range(a, start + q0 + rlo + 8, len);
+    // keys that all sixteen rows of the warp attend: below all_s, and from all_lo to all_hi
+    const KeyRange ka = key_range(a, start + q0 + wrow, len), kz = key_range(a, start + q0 + wrow + 15, len);
+    const int all_s = ka.s, all_lo = kz.lo, all_hi = ka.hi;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    bool ok = true;
+#pragma unroll 2
+    for (int j = 0; j < nkv; ++j) {
+      const int key0 = (j < sink_tiles ? j : first_tile + (j - sink_tiles)) * BKV;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[x], j & 1, err))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float sc[64];
+      tmem_ld_16x256b_x16(lane_addr + s_col, sc);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.s_free[x]);
+      if (!(key0 + BKV <= all_s || (key0 >= all_lo && key0 + BKV <= all_hi))) {
+#pragma unroll
+        for (int g = 0; g < 16; ++g)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = key0 + 8 * g + cq + e;
+            if (key >= k0.hi || (key < k0.lo && key >= k0.s)) sc[4 * g + e] = -INFINITY;
+            if (key >= k1.hi || (key < k1.lo && key >= k1.s)) sc[4 * g + 2 + e] = -INFINITY;
+          }
+      }
+      float p0[4], p1[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        p0[q] = fmaxf(sc[4 * q], sc[4 * q + 1]);
+        p1[q] = fmaxf(sc[4 * q + 2], sc[4 * q + 3]);
+      }
+#pragma unroll
+      for (int g = 4; g < 16; ++g) {
+        p0[g & 3] = max3f(p0[g & 3], sc[4 * g], sc[4 * g + 1]);
+        p1[g & 3] = max3f(p1[g & 3], sc[4 * g + 2], sc[4 * g + 3]);
+      }
+      float mx0 = max3f(p0[0], p0[1], fmaxf(p0[2], p0[3]));
+      float mx1 = max3f(p1[0], p1[1], fmaxf(p1[2], p1[3]));
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2)) * a.scale_log2;
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2)) * a.scale_log2;
+      float c0 = 1.f, c1 = 1.f;
+      if (mx0 > m0 + kRescaleThreshold) {
+        c0 = ex2(m0 - mx0);
+        m0 = mx0;
+      }
+      if (mx1 > m1 + kRescaleThreshold) {
+        c1 = ex2(m1 - mx1);
+        m1 = mx1;
+      }
+      const uint64_t sl2 = f2_pack(a.scale_log2, a.scale_log2);
+      const float n0 = m0 == -INFINITY ? 0.f : -m0, n1 = m1 == -INFINITY ? 0.f : -m1;
+      const uint64_t nb0 = f2_pack(n0, n0), nb1 = f2_pack(n1, n1);
+      if (x == 1 && j == 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.stagger, 0, err))) {
+        ok = false;
+        break;
+      }
+      uint64_t a0[2] = {0ull, 0ull}, a1[2] = {0ull, 0ull};
+      uint32_t pk[32];
+#pragma unroll
+      for (int g = 0; g < 16; ++g) {
+        float e0, e1, e2, e3;
+        f2_unpack(f2_fma(f2_pack(sc[4 * g], sc[4 * g + 1]), sl2, nb0), e0, e1);
+        f2_unpack(f2_fma(f2_pack(sc[4 * g + 2], sc[4 * g + 3]), sl2, nb1), e2, e3);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        e2 = ex2(e2);
+        e3 = ex2(e3);
+        a0[g & 1] = f2_add(a0[g & 1], f2_pack(e0, e1));
+        a1[g & 1] = f2_add(a1[g & 1], f2_pack(e2, e3));
+        // the weights are rounded to bf16 for the tensor cores; their sums are not
+        pk[2 * g] = pack_bf16x2(e0, e1);
+        pk[2 * g + 1] = pack_bf16x2(e2, e3);
+      }
+      if (x == 0 && j == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.stagger);
+      }
+      float s0, s1, s2, s3;
+      f2_unpack(f2_add(a0[0], a0[1]), s0, s1);
+      f2_unpack(f2_add(a1[0], a1[1]), s2, s3);
+      l0 = l0 * c0 + (s0 + s1);
+      l1 = l1 * c1 + (s2 + s3);
+      if (j > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.pv_done[x], (j - 1) & 1, err))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      // V rows of keys that no row of the CTA attends (padding, evicted tokens) become zeros:
+      // their weights are zero, but zero times what they hold need not be.  Tile 0's warps do
+      // it before they release P_0, and both tiles' P V follow that.
+      if (x == 0 && (key0 + BKV > hi || (key0 < lo && key0 + BKV > sink))) {
+        const int s = j % STAGES;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / STAGES) & 1, err))) {
+          ok = false;
+          break;
+        }
+        uint4* v = reinterpret_cast<uint4*>(sKV + s * 2 * KV_BYTES + KV_BYTES);
+        for (int i = threadIdx.x; i < BKV * 8; i += 256) {
+          const int key = key0 + (i >> 3);
+          if (key >= hi || (key < lo && key >= sink)) v[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      tmem_st_16x128b_x16(lane_addr + p_col, pk);
+      if (j > 0 && __any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
+        float o[32];
+        tmem_ld_16x256b_x8(lane_addr + o_col, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          o[4 * g] *= c0;
+          o[4 * g + 1] *= c0;
+          o[4 * g + 2] *= c1;
+          o[4 * g + 3] *= c1;
+        }
+        tmem_st_16x256b_x8(lane_addr + o_col, o);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[x]);
+    }
+    // row sums: the four threads of a row hold disjoint keys
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (__all_sync(0xffffffffu, ok && (nkv == 0 || mbar_wait(&bar.pv_done[x], (nkv - 1) & 1, err)))) {
+      float o[32];
+      if (nkv > 0) {
+        tc_fence_after();
+        tmem_ld_16x256b_x8(lane_addr + o_col, o);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+      }
+      uint32_t redo = 0;     // rows of this warp that came out non-finite
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int tok = q0 + rlo + 8 * rr;
+        // a row with no attended key (l = 0) writes zeros rather than 0 * inf
+        const float lr = rr ? l1 : l0;
+        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        float bad = lr * 0.f;                              // 0, or NaN
+#pragma unroll
+        for (int g = 0; g < 8; ++g) bad += (o[4 * g + 2 * rr] + o[4 * g + 2 * rr + 1]) * 0.f;
+        if (tok < a.n_q) {
+          uint32_t* d32 = reinterpret_cast<uint32_t*>(a.out + (((int64_t)b * a.n_q + tok) * a.heads + h) * 64 + cq);
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            d32[4 * g] = lr == 0.f ? 0u : pack_bf16x2(o[4 * g + 2 * rr] * inv, o[4 * g + 2 * rr + 1] * inv);
+        }
+        uint32_t v = __ballot_sync(0xffffffffu, bad != 0.f && tok < a.n_q);
+        v |= v >> 1;
+        v |= v >> 2;                                       // bit 4 r: row r's four threads
+#pragma unroll
+        for (int r = 0; r < 8; ++r) redo |= ((v >> (4 * r)) & 1u) << (r + 8 * rr);
+      }
+      // A non-finite value in V reaches the whole tile through a weight of zero: such rows
+      // are done again from their attended keys alone.
+      __syncwarp();
+      for (; redo; redo &= redo - 1) {
+        const int i = q0 + wrow + __ffs(redo) - 1;
+        attend_row(a, b, h, i, start + i, len);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 17) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace tc
+
+cudaError_t launch_many(const WindowArgs& a, const RowSpans& spans, int B, int* err, cudaStream_t st) {
+  // [B * heads, n, 64] views: tiles of 128 rows never cross into the next head, and rows
+  // past the end read as zeros
+  CUtensorMap tq, tk, tv;
+  if (!encode_tmap_bf16_3d(&tq, a.q, 64, a.n_q, (uint64_t)B * a.heads, 128) ||
+      !encode_tmap_bf16_3d(&tk, a.k, 64, a.n_kv, (uint64_t)B * a.kv_heads, 128) ||
+      !encode_tmap_bf16_3d(&tv, a.v, 64, a.n_kv, (uint64_t)B * a.kv_heads, 128))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> attr{0};
+  const cudaError_t e = ensure_smem_limit(tc::window_attention_tc_kernel, (int)tc::SMEM, attr);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tc::window_attention_tc_kernel, dim3((a.n_q + 2 * tc::BQ - 1) / (2 * tc::BQ), a.heads, B),
+                    dim3(tc::THREADS), tc::SMEM, st, tq, tk, tv, a, spans, err);
+}
+
+// Up to this many query rows a key head, 16-row tiles; above, 128-row tiles.
+constexpr int kFewRows = 64;
+
 }  // namespace
 
 }  // namespace lens
@@ -320,7 +711,11 @@ extern "C" lens_status lens_op_attention_window(const uint16_t* q, const uint16_
     return LENS_ERR_INVALID_ARG;
   const WindowArgs a{reinterpret_cast<const __nv_bfloat16*>(q), reinterpret_cast<const __nv_bfloat16*>(k),
                      reinterpret_cast<const __nv_bfloat16*>(v), reinterpret_cast<__nv_bfloat16*>(out), heads, kv_heads,
-                     n_q, n_kv, left < 0 || left > kMaxPos ? kMaxPos : left, right < 0 || right > kMaxPos - 1 ? kMaxPos - 1 : right,
-                     sinks, scale * 1.4426950408889634f};
-  return launch_few(a, spans, B, (cudaStream_t)stream) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
+                     n_q, n_kv, left < 0 || left > kMaxPos ? kMaxPos : left,
+                     right < 0 || right > kMaxPos ? kMaxPos : right, sinks, scale * 1.4426950408889634f};
+  cudaStream_t st = (cudaStream_t)stream;
+  if (n_q <= kFewRows) return launch_few(a, spans, B, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
+  int* err = op_err_ptr();
+  if (!err) return LENS_ERR_CUDA;
+  return launch_many(a, spans, B, err, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
 }

@@ -413,7 +413,7 @@ LENS_API lens_status lens_op_sandwich_norm(const float* h, const void* y, lens_d
  * most 1024; q, k, v, out 16-byte aligned; out must not overlap q, k or v.
  * Errors: INVALID_ARG (NULL, misaligned, scale not finite or <= 0, left or right < -1,
  * sinks < 0), SHAPE (B, heads, kv_heads, n_q, n_kv < 1, lengths or starts out of range,
- * q_start + n_q or n_kv > 2^30). */
+ * q_start + n_q or n_kv > 2^29). */
 LENS_API lens_status lens_op_attention_window(const uint16_t* q, const uint16_t* k, const uint16_t* v, int B, int heads,
                                               int kv_heads, int n_q, int n_kv, const int* q_start, const int* kv_len,
                                               int left, int right, int sinks, float scale, uint16_t* out,

@@ -66,8 +66,8 @@ def test_attention_window_refusals(lib):
                dict(right=-2), dict(sinks=-1)):
         assert call(**kw) == BAD, kw
     for kw in (dict(b=0), dict(b=65), dict(h=0), dict(h=1025, hk=1025), dict(hk=0), dict(h=4, hk=3), dict(nq=0),
-               dict(nkv=0), dict(nkv=2 ** 30 + 1), dict(nq=2 ** 30 + 1), dict(start=[0, -1]),
-               dict(start=[2 ** 30, 0]), dict(length=[10, 1]), dict(length=[-1, 1])):
+               dict(nkv=0), dict(nkv=2 ** 29 + 1), dict(nq=2 ** 29 + 1), dict(start=[0, -1]),
+               dict(start=[2 ** 29 - 4, 0]), dict(length=[10, 1]), dict(length=[-1, 1])):
         assert call(**kw) == SHAPE, kw
 
 
