@@ -20,24 +20,43 @@ namespace {
 // stay in the tensor cores' accumulator: each block's P_g goes to its own TMEM slot
 // (SLOTS of them in turn) and eight epilogue warps read it, scale it and add it to the
 // tile's sum in registers (BN / 2 a thread) while the tensor cores work on the next.
-//   warp 0      TMA: 128 rows of A and BN / 2 rows of W of each k block (128-byte rows)
-//   warp 1      MMA issuer (leader CTA): 4 x (M = 256, N = BN, K = 32) into a slot
-//   warps 2..9  scale and add, then the tile's output through shared memory by TMA
+//   warp 0       TMA: 128 rows of A and BN / 2 rows of W of each k block (128-byte rows)
+//   warps 1, 10  MMA issuers (leader CTA) of the even and the odd k blocks: 4 x (M = 256,
+//                N = BN, K = 32) into a slot.  Blocks do not depend on each other, and one
+//                thread's two waits, four MMAs and two commits a block took longer than
+//                the MMAs themselves.
+//   warps 2..9   scale and add, then the tile's output through shared memory by TMA
+//   warp 11      copies a block's scales beside its slot (cp.async), so that no load's
+//                latency and no address arithmetic is on the adding warps' way
 //   full[s]    (leader)  TMA bytes of both CTAs
 //   empty[s]   (both)    the k block's MMAs are done: stage s may be refilled
-//   tfull[a]   (both)    slot a holds a k block's P_g
+//   tfull[a]   (both)    slot a holds a k block's P_g, and its scales have landed
 //   tempty[a]  (leader)  both CTAs' epilogue warps have read slot a
+//   sfree[a]   (each)    this CTA's epilogue warps have read slot a's scales
 template <int BN>
 struct F8Cfg {
   static constexpr int BK = 128;
   static constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = (BN / 2) * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int EPI_WARPS = 8, THREADS = 384;
   static constexpr uint32_t EPI_SLOT = 4096, EPI_BYTES = EPI_WARPS * EPI_SLOT;
-  static constexpr uint32_t BUDGET = 232448 - 1024 - 256 - EPI_BYTES;
-  static constexpr int STAGES = BUDGET / STAGE_BYTES > 8 ? 8 : BUDGET / STAGE_BYTES;
   static constexpr int SLOTS = 512 / BN;
-  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_BYTES + 256;
+  static constexpr int SCALES = 132;                      // of a slot: 128 rows, then two column blocks
+  static constexpr uint32_t SCALE_BYTES = SLOTS * SCALES * 4;
+  static constexpr uint32_t BUDGET = 232448 - 1024 - 512 - EPI_BYTES - SCALE_BYTES;
+  static constexpr int STAGES = BUDGET / STAGE_BYTES > 8 ? 8 : BUDGET / STAGE_BYTES;
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_BYTES + SCALE_BYTES + 512;
 };
+
+// 4 bytes global -> shared without registers; zero when !live
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrive once on `bar` (an arrival its count includes) when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 struct F8GemmArgs {
   int M, N, kblocks, tiles_m, total_tiles, nblocks;
@@ -56,14 +75,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
   uint8_t* sA = smem;
   uint8_t* sW = smem + STAGES * C::A_BYTES;
   uint8_t* sEpi = sW + STAGES * C::B_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES);
+  float* sScale = reinterpret_cast<float*>(sEpi + C::EPI_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES + C::SCALE_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + SLOTS;
-  uint64_t* drain = tempty + SLOTS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* sfree = tempty + SLOTS;
+  uint64_t* drain = sfree + SLOTS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   uint32_t* peer_issued = tmem_slot + 1;
-  static_assert((2 * STAGES + 2 * SLOTS + 1) * 8 + 8 <= 256, "barriers overflow their reserve");
+  static_assert((2 * STAGES + 3 * SLOTS + 2) * 8 + 8 <= 512, "barriers overflow their reserve");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -75,10 +96,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(&tfull[s], 1);
+      mbar_init(&tfull[s], 1 + 32);
       mbar_init(&tempty[s], 2 * C::EPI_WARPS);
+      mbar_init(&sfree[s], C::EPI_WARPS);
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *peer_issued = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
@@ -121,36 +144,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
       if (rank == 1) st_shared_cluster_u32(mapa_shared(smem_u32(peer_issued), 0), prod_issued);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 10) {
     if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc = umma_idesc_e4m3(256, BN);
-      uint32_t stage = 0, phase = 0, slot = 0, use = 0;
+      const uint32_t odd = warp == 10;
       bool ok = true;
-      for (int t = pair; t < a.total_tiles && ok; t += npairs) {
-        for (int kb = 0; kb < a.kblocks; ++kb) {
-          if (!mbar_wait_sleep(&tempty[slot], use ^ 1, a.err) || !mbar_wait_sleep(&full[stage], phase, a.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = umma_desc_sw128(smem_u32(sA + stage * C::A_BYTES));
-          const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * C::B_BYTES));
+      uint32_t stage = odd, phase = 0, slot = odd, use = 0;
+      // this thread's k blocks in the pair's sequence of them: every second one
+      const int64_t steps = (int64_t)((a.total_tiles - pair + npairs - 1) / npairs) * a.kblocks;
+      for (int64_t i = odd; i < steps; i += 2) {
+        if (!mbar_wait_sleep(&tempty[slot], use ^ 1, a.err) || !mbar_wait_sleep(&full[stage], phase, a.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t ad = umma_desc_sw128(smem_u32(sA + stage * C::A_BYTES));
+        const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * C::B_BYTES));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + slot * BN, ad + 2 * k, wd + 2 * k, idesc, k > 0 ? 1u : 0u);
-          umma_commit_pair(&empty[stage], 0x3);
-          umma_commit_pair(&tfull[slot], 0x3);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
-          if (++slot == SLOTS) {
-            slot = 0;
-            use ^= 1;
-          }
+        for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + slot * BN, ad + 2 * k, wd + 2 * k, idesc, k > 0 ? 1u : 0u);
+        umma_commit_pair(&empty[stage], 0x3);
+        umma_commit_pair(&tfull[slot], 0x3);
+        if ((stage += 2) >= STAGES) {
+          stage -= STAGES;
+          phase ^= 1;
+        }
+        if ((slot += 2) >= SLOTS) {
+          slot -= SLOTS;
+          use ^= 1;
         }
       }
-      if (!ok) umma_drain_pair(drain);
+      if (!ok) umma_drain_pair(&drain[odd]);
     }
+    __syncwarp();
+  } else if (warp == 11) {
+    uint32_t slot = 0, use = 0;
+    bool ok = true;
+    for (int t = pair; t < a.total_tiles && ok; t += npairs) {
+      const int tn = t / a.tiles_m, row = (t - tn * a.tiles_m) * 256 + 128 * (int)rank + lane;
+      const float* pa = a.as + row;
+      // a column block past the last one holds no output: any block's scale will do
+      const float* pw = a.ws + min(tn * BN / kF8Group + (BN > 128 ? lane & 1 : 0), a.nblocks - 1);
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sfree[slot], use ^ 1, a.err))) {
+          ok = false;
+          break;
+        }
+        float* dst = sScale + slot * C::SCALES;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool live = row + 32 * i < a.M;
+          cp_async4(dst + lane + 32 * i, live ? pa + 32 * i : a.as, live);
+        }
+        if (lane < 2) cp_async4(dst + 128 + lane, pw, true);
+        cp_async_arrive(&tfull[slot]);
+        pa += a.M;
+        pw += a.nblocks;
+        if (++slot == SLOTS) {
+          slot = 0;
+          use ^= 1;
+        }
+      }
+    }
+    cp_async_wait_all();
     __syncwarp();
   } else {
     const int quarter = warp & 3, part = (warp - 2) >> 2;
@@ -158,45 +213,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
     const uint32_t leader_tempty = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t lane_addr = tmem + (uint32_t(quarter * 32) << 16) + part * COLS;
     uint32_t slot = 0, use = 0, no_slot = 0;
-    bool ok = true;
+    bool ok = true, ready = false;
+    const float* a_scale = sScale + quarter * 32 + lane;
+    const float* w_scale = sScale + 128 + part;     // (the same block twice where BN = 128)
     for (int t = pair; t < a.total_tiles && ok; t += npairs) {
-      const int row0 = (t % a.tiles_m) * 256 + 128 * (int)rank + quarter * 32, row = row0 + lane;
+      const int row0 = (t % a.tiles_m) * 256 + 128 * (int)rank + quarter * 32;
       const int n0 = (t / a.tiles_m) * BN + part * COLS;
-      const bool live = row < a.M;
-      const float* as = a.as + row;
-      // a column block past the last one holds no output: any block's scale will do
-      const float* ws = a.ws + min(n0 / kF8Group, a.nblocks - 1);
       uint64_t acc[COLS / 2];
 #pragma unroll
       for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
-      // scales of the next k block, loaded one block ahead
-      float s_next = live ? __ldg(as) * __ldg(ws) : 0.f;
 #pragma unroll 1
       for (int kb = 0; kb < a.kblocks; ++kb) {
-        const float s = s_next;
-        if (live && kb + 1 < a.kblocks)
-          s_next = __ldg(as + (int64_t)(kb + 1) * a.M) * __ldg(ws + (int64_t)(kb + 1) * a.nblocks);
-        const uint64_t s2 = f2_pack(s, s);
-        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[slot], use, a.err))) {
+        if (!__all_sync(0xffffffffu, ready) && !__all_sync(0xffffffffu, mbar_wait(&tfull[slot], use, a.err))) {
           ok = false;
           break;
         }
         tc_fence_after();
+        // the load of one 16-column piece runs while the one before it is added
+        const uint32_t at = lane_addr + slot * BN;
+        float r[2][16];
+        tmem_ld16(at, r[0]);
+        const float s = a_scale[slot * C::SCALES] * w_scale[slot * C::SCALES];
+        const uint64_t s2 = f2_pack(s, s);
 #pragma unroll
-        for (int c = 0; c < COLS / 32; ++c) {
-          float r[32];
-          tmem_ld32(lane_addr + slot * BN + 32 * c, r);
-          tmem_ld_wait();
+        for (int c = 0; c < COLS / 16; ++c) {
+          tmem_ld_wait(r[c & 1]);
+          if (c + 1 < COLS / 16) {
+            tmem_ld16(at + 16 * (c + 1), r[(c + 1) & 1]);
+          } else {
+            // everything is in registers: the slot may be filled again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_remote(leader_tempty + slot * 8);
+              mbar_arrive(&sfree[slot]);
+            }
+            if (++slot == SLOTS) {
+              slot = 0;
+              use ^= 1;
+            }
+            ready = mbar_test(&tfull[slot], use);    // asked ahead of the adds that hide it
+          }
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[16 * c + i] = f2_fma(f2_pack(r[2 * i], r[2 * i + 1]), s2, acc[16 * c + i]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader_tempty + slot * 8);
-        if (++slot == SLOTS) {
-          slot = 0;
-          use ^= 1;
+          for (int i = 0; i < 8; ++i)
+            acc[8 * c + i] = f2_fma(f2_pack(r[c & 1][2 * i], r[c & 1][2 * i + 1]), s2, acc[8 * c + i]);
         }
       }
       if (!ok) break;
