@@ -15,14 +15,14 @@ namespace lens {
 namespace {
 
 // ------------------------------------------------------------------ tcgen05, CTA pairs
-// 256 x BN tiles by a cluster of two CTAs (cta_group::2, kind::f8f6f4), persistent.
+// 256 x 128 tiles by a cluster of two CTAs (cta_group::2, kind::f8f6f4), persistent.
 // The scales differ from one 128-wide k block to the next, so a tile's sum over k cannot
 // stay in the tensor cores' accumulator: each block's P_g goes to its own TMEM slot
-// (SLOTS of them in turn) and eight epilogue warps read it, scale it and add it to the
-// tile's sum in registers (BN / 2 a thread) while the tensor cores work on the next.
-//   warp 0       TMA: 128 rows of A and BN / 2 rows of W of each k block (128-byte rows)
+// (four of them in turn) and eight epilogue warps read it, scale it and add it to the
+// tile's sum in registers (64 a thread) while the tensor cores work on the next.
+//   warp 0       TMA: 128 rows of A and 64 rows of W of each k block (128-byte rows)
 //   warps 1, 10  MMA issuers (leader CTA) of the even and the odd k blocks: 4 x (M = 256,
-//                N = BN, K = 32) into a slot.  Blocks do not depend on each other, and one
+//                N = 128, K = 32) into a slot.  Blocks do not depend on each other, and one
 //                thread's two waits, four MMAs and two commits a block took longer than
 //                the MMAs themselves.
 //   warps 2..9   scale and add, then the tile's output through shared memory by TMA
@@ -33,19 +33,17 @@ namespace {
 //   tfull[a]   (both)    slot a holds a k block's P_g, and its scales have landed
 //   tempty[a]  (leader)  both CTAs' epilogue warps have read slot a
 //   sfree[a]   (each)    this CTA's epilogue warps have read slot a's scales
-template <int BN>
-struct F8Cfg {
-  static constexpr int BK = 128;
-  static constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = (BN / 2) * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int EPI_WARPS = 8, THREADS = 384;
-  static constexpr uint32_t EPI_SLOT = 4096, EPI_BYTES = EPI_WARPS * EPI_SLOT;
-  static constexpr int SLOTS = 512 / BN;
-  static constexpr int SCALES = 132;                      // of a slot: 128 rows, then two column blocks
-  static constexpr uint32_t SCALE_BYTES = SLOTS * SCALES * 4;
-  static constexpr uint32_t BUDGET = 232448 - 1024 - 512 - EPI_BYTES - SCALE_BYTES;
-  static constexpr int STAGES = BUDGET / STAGE_BYTES > 8 ? 8 : BUDGET / STAGE_BYTES;
-  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_BYTES + SCALE_BYTES + 512;
-};
+constexpr int BN = 128, BK = 128, COLS = BN / 2;          // COLS: columns a thread accumulates
+constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = (BN / 2) * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int EPI_WARPS = 8, THREADS = 384;
+constexpr uint32_t EPI_SLOT = 4096, EPI_BYTES = EPI_WARPS * EPI_SLOT;
+constexpr int SLOTS = 512 / BN;
+constexpr int SCALES = 132;                               // of a slot: 128 rows, the column block (16-byte multiple)
+constexpr uint32_t SCALE_BYTES = SLOTS * SCALES * 4;
+constexpr int STAGES = 7;
+constexpr uint32_t BAR_BYTES = 512;
+constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_BYTES + SCALE_BYTES + BAR_BYTES;
+static_assert(SMEM <= 232448, "shared memory");
 
 // 4 bytes global -> shared without registers; zero when !live
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool live) {
@@ -64,19 +62,17 @@ struct F8GemmArgs {
   int* err;
 };
 
-template <int BN, bool BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 1)
+template <bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     gemm_f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmC, const F8GemmArgs a) {
-  using C = F8Cfg<BN>;
-  constexpr int STAGES = C::STAGES, SLOTS = C::SLOTS, COLS = BN / 2;   // columns a thread accumulates
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
-  uint8_t* sW = smem + STAGES * C::A_BYTES;
-  uint8_t* sEpi = sW + STAGES * C::B_BYTES;
-  float* sScale = reinterpret_cast<float*>(sEpi + C::EPI_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES + C::SCALE_BYTES);
+  uint8_t* sW = smem + STAGES * A_BYTES;
+  uint8_t* sEpi = sW + STAGES * B_BYTES;
+  float* sScale = reinterpret_cast<float*>(sEpi + EPI_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + EPI_BYTES + SCALE_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + SLOTS;
@@ -84,7 +80,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
   uint64_t* drain = sfree + SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   uint32_t* peer_issued = tmem_slot + 1;
-  static_assert((2 * STAGES + 3 * SLOTS + 2) * 8 + 8 <= 512, "barriers overflow their reserve");
+  static_assert((2 * STAGES + 3 * SLOTS + 2) * 8 + 8 <= BAR_BYTES, "barriers overflow their reserve");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -97,8 +93,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
     }
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&tfull[s], 1 + 32);
-      mbar_init(&tempty[s], 2 * C::EPI_WARPS);
-      mbar_init(&sfree[s], C::EPI_WARPS);
+      mbar_init(&tempty[s], 2 * EPI_WARPS);
+      mbar_init(&sfree[s], EPI_WARPS);
     }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
@@ -130,9 +126,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
             prod_ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
-          tma_load_2d_pair(sA + stage * C::A_BYTES, &tmA, &full[stage], kb * C::BK, m0);
-          tma_load_2d_pair(sW + stage * C::B_BYTES, &tmW, &full[stage], kb * C::BK, n0);
+          if (rank == 0) mbar_expect_tx(&full[stage], 2 * STAGE_BYTES);
+          tma_load_2d_pair(sA + stage * A_BYTES, &tmA, &full[stage], kb * BK, m0);
+          tma_load_2d_pair(sW + stage * B_BYTES, &tmW, &full[stage], kb * BK, n0);
           ++prod_issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -158,8 +154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
           break;
         }
         tc_fence_after();
-        const uint64_t ad = umma_desc_sw128(smem_u32(sA + stage * C::A_BYTES));
-        const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * C::B_BYTES));
+        const uint64_t ad = umma_desc_sw128(smem_u32(sA + stage * A_BYTES));
+        const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * B_BYTES));
 #pragma unroll
         for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + slot * BN, ad + 2 * k, wd + 2 * k, idesc, k > 0 ? 1u : 0u);
         umma_commit_pair(&empty[stage], 0x3);
@@ -182,20 +178,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
     for (int t = pair; t < a.total_tiles && ok; t += npairs) {
       const int tn = t / a.tiles_m, row = (t - tn * a.tiles_m) * 256 + 128 * (int)rank + lane;
       const float* pa = a.as + row;
-      // a column block past the last one holds no output: any block's scale will do
-      const float* pw = a.ws + min(tn * BN / kF8Group + (BN > 128 ? lane & 1 : 0), a.nblocks - 1);
+      const float* pw = a.ws + tn;             // a tile's columns are one block of W's scales
       for (int kb = 0; kb < a.kblocks; ++kb) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sfree[slot], use ^ 1, a.err))) {
           ok = false;
           break;
         }
-        float* dst = sScale + slot * C::SCALES;
+        float* dst = sScale + slot * SCALES;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool live = row + 32 * i < a.M;
           cp_async4(dst + lane + 32 * i, live ? pa + 32 * i : a.as, live);
         }
-        if (lane < 2) cp_async4(dst + 128 + lane, pw, true);
+        if (lane == 0) cp_async4(dst + 128, pw, true);
         cp_async_arrive(&tfull[slot]);
         pa += a.M;
         pw += a.nblocks;
@@ -209,13 +204,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
     __syncwarp();
   } else {
     const int quarter = warp & 3, part = (warp - 2) >> 2;
-    uint8_t* box = sEpi + (warp - 2) * C::EPI_SLOT;
+    uint8_t* box = sEpi + (warp - 2) * EPI_SLOT;
     const uint32_t leader_tempty = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t lane_addr = tmem + (uint32_t(quarter * 32) << 16) + part * COLS;
     uint32_t slot = 0, use = 0, no_slot = 0;
     bool ok = true, ready = false;
     const float* a_scale = sScale + quarter * 32 + lane;
-    const float* w_scale = sScale + 128 + part;     // (the same block twice where BN = 128)
+    const float* w_scale = sScale + 128;
     for (int t = pair; t < a.total_tiles && ok; t += npairs) {
       const int row0 = (t % a.tiles_m) * 256 + 128 * (int)rank + quarter * 32;
       const int n0 = (t / a.tiles_m) * BN + part * COLS;
@@ -229,35 +224,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
           break;
         }
         tc_fence_after();
-        // the load of one 16-column piece runs while the one before it is added
-        const uint32_t at = lane_addr + slot * BN;
-        float r[2][16];
-        tmem_ld16(at, r[0]);
-        const float s = a_scale[slot * C::SCALES] * w_scale[slot * C::SCALES];
+        float r[2][32];
+        tmem_ld32(lane_addr + slot * BN, r[0]);
+        tmem_ld32(lane_addr + slot * BN + 32, r[1]);
+        const float s = a_scale[slot * SCALES] * w_scale[slot * SCALES];
         const uint64_t s2 = f2_pack(s, s);
-#pragma unroll
-        for (int c = 0; c < COLS / 16; ++c) {
-          tmem_ld_wait(r[c & 1]);
-          if (c + 1 < COLS / 16) {
-            tmem_ld16(at + 16 * (c + 1), r[(c + 1) & 1]);
-          } else {
-            // everything is in registers: the slot may be filled again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_remote(leader_tempty + slot * 8);
-              mbar_arrive(&sfree[slot]);
-            }
-            if (++slot == SLOTS) {
-              slot = 0;
-              use ^= 1;
-            }
-            ready = mbar_test(&tfull[slot], use);    // asked ahead of the adds that hide it
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc[8 * c + i] = f2_fma(f2_pack(r[c & 1][2 * i], r[c & 1][2 * i + 1]), s2, acc[8 * c + i]);
+        tmem_ld_wait(r[0]);
+        tmem_ld_pin(r[1]);
+        // everything is in registers: the slot may be filled again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_remote(leader_tempty + slot * 8);
+          mbar_arrive(&sfree[slot]);
         }
+        if (++slot == SLOTS) {
+          slot = 0;
+          use ^= 1;
+        }
+        ready = mbar_test(&tfull[slot], use);    // asked ahead of the adds that hide it
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[16 * c + i] = f2_fma(f2_pack(r[c][2 * i], r[c][2 * i + 1]), s2, acc[16 * c + i]);
       }
       if (!ok) break;
       constexpr int PER = BF16 ? 64 : 32;        // columns of one 128-byte box row
@@ -292,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
   tc_fence_before();
   cluster_sync_all();          // every role of both CTAs has left its loop
   if (warp == 0 && lane == 0 && rank == 0 && (!prod_ok || err_raised(a.err)))
-    drain_pair_stages<STAGES>(full, [&](uint32_t) { return C::STAGE_BYTES; }, prod_issued, *peer_issued);
+    drain_pair_stages<STAGES>(full, [&](uint32_t) { return STAGE_BYTES; }, prod_issued, *peer_issued);
   cluster_sync_all();          // no MMA, TMA or remote arrive of the pair is in flight
   if (warp == 1) {
     tc_fence_after();
@@ -300,15 +290,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8Cfg<BN>::THREADS, 
   }
 }
 
-template <int BN, bool BF16>
+template <bool BF16>
 cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
-  using C = F8Cfg<BN>;
   CUtensorMap ta, tw, tc;
   if (!encode_tmap_u8(&ta, g.A, g.M, g.K, 128) || !encode_tmap_u8(&tw, g.W, g.N, g.K, BN / 2) ||
       !encode_tmap_out(&tc, g.C, BF16 ? 2 : 4, g.M, g.N, g.N))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> attr{0};
-  const cudaError_t e = ensure_smem_limit(gemm_f8_pair_kernel<BN, BF16>, (int)C::SMEM, attr);
+  const cudaError_t e = ensure_smem_limit(gemm_f8_pair_kernel<BF16>, (int)SMEM, attr);
   if (e != cudaSuccess) return e;
   F8GemmArgs a;
   a.M = g.M;
@@ -322,15 +311,13 @@ cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
   a.bias = g.bias;
   a.err = err;
   const int pairs = a.total_tiles < sms / 2 ? a.total_tiles : sms / 2;
-  return launch_pdl(gemm_f8_pair_kernel<BN, BF16>, dim3(2 * pairs), dim3(C::THREADS), C::SMEM, st, ta, tw, tc, a);
+  return launch_pdl(gemm_f8_pair_kernel<BF16>, dim3(2 * pairs), dim3(THREADS), SMEM, st, ta, tw, tc, a);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_f8(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
-  const int64_t wide = ((g.M + 255) / 256) * (int64_t)((g.N + 255) / 256);
-  if (wide >= sms / 2) return g.bf16 ? launch_pair<256, true>(g, err, sms, st) : launch_pair<256, false>(g, err, sms, st);
-  return g.bf16 ? launch_pair<128, true>(g, err, sms, st) : launch_pair<128, false>(g, err, sms, st);
+  return g.bf16 ? launch_pair<true>(g, err, sms, st) : launch_pair<false>(g, err, sms, st);
 }
 
 }  // namespace lens

@@ -410,14 +410,19 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// The same, naming the registers of the load waited for, so that nothing that reads them
-// can be scheduled ahead of the wait.
-__device__ __forceinline__ void tmem_ld_wait(float (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
+// The same, naming registers of the loads waited for, so that nothing that reads them can be
+// scheduled ahead of the wait (tmem_ld_pin: more registers of the same loads, after it).
+__device__ __forceinline__ void tmem_ld_pin(float (&r)[32]) {
+  asm volatile(""
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
-               :
-               : "memory");
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]),
+                 "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]),
+                 "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]),
+                 "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]));
+}
+__device__ __forceinline__ void tmem_ld_wait(float (&r)[32]) {
+  tmem_ld_wait();
+  tmem_ld_pin(r);
 }
 
 // 32 lanes x 32 consecutive fp32 columns from registers; thread i writes lane (base + i).
