@@ -15,35 +15,38 @@ namespace lens {
 namespace {
 
 // ------------------------------------------------------------------ tcgen05, CTA pairs
-// 256 x 128 tiles by a cluster of two CTAs (cta_group::2, kind::f8f6f4), persistent.
-// The scales differ from one 128-wide k block to the next, so a tile's sum over k cannot
-// stay in the tensor cores' accumulator: each block's P_g goes to its own TMEM slot
-// (four of them in turn) and eight epilogue warps read it, scale it and add it to the
+// 256 x 128 tiles by a cluster of two CTAs (cta_group::2, kind::f8f6f4), persistent.  The
+// scales differ from one 128-wide k block to the next, so a tile's sum over
+// k cannot stay in the tensor cores' accumulator: each block's P_g goes to its own TMEM slot
+// (four of them in turn), and eight epilogue warps read it, scale it and add it to the
 // tile's sum in registers (64 a thread) while the tensor cores work on the next.
 //   warp 0       TMA: 128 rows of A and 64 rows of W of each k block (128-byte rows)
-//   warps 1, 10  MMA issuers (leader CTA) of the even and the odd k blocks: 4 x (M = 256,
-//                N = 128, K = 32) into a slot.  Blocks do not depend on each other, and one
-//                thread's two waits, four MMAs and two commits a block took longer than
-//                the MMAs themselves.
-//   warps 2..9   scale and add, then the tile's output through shared memory by TMA
-//   warp 11      copies a block's scales beside its slot (cp.async), so that no load's
+//   warps 1, 2   MMA issuers (leader CTA) of the even and the odd k blocks: 4 x (M = 256,
+//                N = 128, K = 32) into a slot.  Blocks do not depend on each other,
+//                and one thread's two waits, four MMAs and two commits a block take longer
+//                than the MMAs themselves.
+//   warp 3       copies a block's scales beside its slot (cp.async), so that no load's
 //                latency and no address arithmetic is on the adding warps' way
+//   warps 4..11  scale and add, then the tile's output through shared memory by TMA; two
+//                warps a TMEM lane quarter, each with half of the tile's columns
 //   full[s]    (leader)  TMA bytes of both CTAs
 //   empty[s]   (both)    the k block's MMAs are done: stage s may be refilled
-//   tfull[a]   (both)    slot a holds a k block's P_g, and its scales have landed
-//   tempty[a]  (leader)  both CTAs' epilogue warps have read slot a
-//   sfree[a]   (each)    this CTA's epilogue warps have read slot a's scales
-constexpr int BN = 128, BK = 128, COLS = BN / 2;          // COLS: columns a thread accumulates
-constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = (BN / 2) * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int EPI_WARPS = 8, THREADS = 384;
-constexpr uint32_t EPI_SLOT = 4096, EPI_BYTES = EPI_WARPS * EPI_SLOT;
-constexpr int SLOTS = 512 / BN;
-constexpr int SCALES = 132;                               // of a slot: 128 rows, the column block (16-byte multiple)
-constexpr uint32_t SCALE_BYTES = SLOTS * SCALES * 4;
-constexpr int STAGES = 7;
-constexpr uint32_t BAR_BYTES = 512;
+//   tfull[j]   (both)    slot j holds a k block's P_g, and its scales have landed
+//   tempty[j]  (leader)  both CTAs' epilogue warps have read slot j
+//   sfree[j]   (each)    this CTA's epilogue warps have read slot j's scales
+// Measured at 8704 x 8192 x 1536: 118 us.  Per k block and pair that is 330 ns: the MMAs
+// alone would take 150, and L2 delivers a pair's 48 KB in 230 (10 TB/s, as for the bf16
+// products); the rest is the way through a slot (MMA, commit, read, release, next MMA), of
+// which four run at a time.  256 x 256 tiles halve W's traffic but leave two slots and gain
+// 5 % at that size and lose 10 to 40 % below it, so there is one tile shape.
+constexpr int BN = 128, COLS = BN / 2;                // COLS: columns a thread accumulates
+constexpr uint32_t A_BYTES = 128 * 128, B_BYTES = (BN / 2) * 128, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGES = 7, SLOTS = 512 / BN;
+constexpr int SCALES = 132;                           // of a slot: 128 rows, the column block
+constexpr uint32_t EPI_BYTES = 8 * 4096, SCALE_BYTES = SLOTS * SCALES * 4, BAR_BYTES = 512;
 constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_BYTES + SCALE_BYTES + BAR_BYTES;
 static_assert(SMEM <= 232448, "shared memory");
+constexpr int THREADS = 384;
 
 // 4 bytes global -> shared without registers; zero when !live
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool live) {
@@ -91,10 +94,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(&tfull[s], 1 + 32);
-      mbar_init(&tempty[s], 2 * EPI_WARPS);
-      mbar_init(&sfree[s], EPI_WARPS);
+    for (int j = 0; j < SLOTS; ++j) {
+      mbar_init(&tfull[j], 1 + 32);
+      mbar_init(&tempty[j], 16);
+      mbar_init(&sfree[j], 8);
     }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
@@ -120,15 +123,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
       for (int t = pair; t < a.total_tiles && prod_ok; t += npairs) {
-        const int m0 = (t % a.tiles_m) * 256 + 128 * (int)rank, n0 = (t / a.tiles_m) * BN + (BN / 2) * (int)rank;
+        const int tn = t / a.tiles_m, m0 = (t - tn * a.tiles_m) * 256 + 128 * (int)rank, n0 = tn * BN + (BN / 2) * (int)rank;
         for (int kb = 0; kb < a.kblocks; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, a.err)) {
             prod_ok = false;
             break;
           }
           if (rank == 0) mbar_expect_tx(&full[stage], 2 * STAGE_BYTES);
-          tma_load_2d_pair(sA + stage * A_BYTES, &tmA, &full[stage], kb * BK, m0);
-          tma_load_2d_pair(sW + stage * B_BYTES, &tmW, &full[stage], kb * BK, n0);
+          tma_load_2d_pair(sA + stage * A_BYTES, &tmA, &full[stage], kb * 128, m0);
+          tma_load_2d_pair(sW + stage * B_BYTES, &tmW, &full[stage], kb * 128, n0);
           ++prod_issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -140,15 +143,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (rank == 1) st_shared_cluster_u32(mapa_shared(smem_u32(peer_issued), 0), prod_issued);
     }
     __syncwarp();
-  } else if (warp == 1 || warp == 10) {
+  } else if (warp == 1 || warp == 2) {
     if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc = umma_idesc_e4m3(256, BN);
-      const uint32_t odd = warp == 10;
+      const uint32_t odd = warp == 2;
       bool ok = true;
       uint32_t stage = odd, phase = 0, slot = odd, use = 0;
-      // this thread's k blocks in the pair's sequence of them: every second one
-      const int64_t steps = (int64_t)((a.total_tiles - pair + npairs - 1) / npairs) * a.kblocks;
-      for (int64_t i = odd; i < steps; i += 2) {
+      const int64_t blocks = (int64_t)((a.total_tiles - pair + npairs - 1) / npairs) * a.kblocks;
+      for (int64_t i = odd; i < blocks; i += 2) {
         if (!mbar_wait_sleep(&tempty[slot], use ^ 1, a.err) || !mbar_wait_sleep(&full[stage], phase, a.err)) {
           ok = false;
           break;
@@ -172,7 +174,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!ok) umma_drain_pair(&drain[odd]);
     }
     __syncwarp();
-  } else if (warp == 11) {
+  } else if (warp == 3) {
     uint32_t slot = 0, use = 0;
     bool ok = true;
     for (int t = pair; t < a.total_tiles && ok; t += npairs) {
@@ -203,17 +205,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     cp_async_wait_all();
     __syncwarp();
   } else {
-    const int quarter = warp & 3, part = (warp - 2) >> 2;
-    uint8_t* box = sEpi + (warp - 2) * EPI_SLOT;
-    const uint32_t leader_tempty = mapa_shared(smem_u32(&tempty[0]), 0);
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
+    uint8_t* box = sEpi + (warp - 4) * 4096;
     const uint32_t lane_addr = tmem + (uint32_t(quarter * 32) << 16) + part * COLS;
-    uint32_t slot = 0, use = 0, no_slot = 0;
-    bool ok = true, ready = false;
+    const uint32_t leader_tempty = mapa_shared(smem_u32(&tempty[0]), 0);
     const float* a_scale = sScale + quarter * 32 + lane;
     const float* w_scale = sScale + 128;
+    uint32_t slot = 0, use = 0, no_box = 0;
+    bool ok = true, ready = false;
     for (int t = pair; t < a.total_tiles && ok; t += npairs) {
-      const int row0 = (t % a.tiles_m) * 256 + 128 * (int)rank + quarter * 32;
-      const int n0 = (t / a.tiles_m) * BN + part * COLS;
       uint64_t acc[COLS / 2];
 #pragma unroll
       for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
@@ -224,9 +224,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           break;
         }
         tc_fence_after();
+        const uint32_t at = lane_addr + slot * BN;
         float r[2][32];
-        tmem_ld32(lane_addr + slot * BN, r[0]);
-        tmem_ld32(lane_addr + slot * BN + 32, r[1]);
+        tmem_ld32(at, r[0]);
+        tmem_ld32(at + 32, r[1]);
         const float s = a_scale[slot * SCALES] * w_scale[slot * SCALES];
         const uint64_t s2 = f2_pack(s, s);
         tmem_ld_wait(r[0]);
@@ -244,12 +245,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         ready = mbar_test(&tfull[slot], use);    // asked ahead of the adds that hide it
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[16 * c + i] = f2_fma(f2_pack(r[c][2 * i], r[c][2 * i + 1]), s2, acc[16 * c + i]);
+        for (int i = 0; i < 32; ++i)
+          acc[i] = f2_fma(f2_pack(r[i / 16][2 * (i % 16)], r[i / 16][2 * (i % 16) + 1]), s2, acc[i]);
       }
       if (!ok) break;
+      const int tn = t / a.tiles_m, row0 = (t - tn * a.tiles_m) * 256 + 128 * (int)rank + quarter * 32;
+      const int n0 = tn * BN + part * COLS;
       constexpr int PER = BF16 ? 64 : 32;        // columns of one 128-byte box row
 #pragma unroll
       for (int c = 0; c < COLS / PER; ++c) {
@@ -272,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             ch[j] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                                __float_as_uint(v[3]));
         }
-        stage_and_ship<false, 1>(box, no_slot, ch, &tmC, n, row0, row0 < a.M && n < a.N);
+        stage_and_ship<false, 1>(box, no_box, ch, &tmC, n, row0, row0 < a.M && n < a.N);
       }
     }
     if (lane == 0) bulk_wait_read<0>();
@@ -293,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 template <bool BF16>
 cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
   CUtensorMap ta, tw, tc;
-  if (!encode_tmap_u8(&ta, g.A, g.M, g.K, 128) || !encode_tmap_u8(&tw, g.W, g.N, g.K, BN / 2) ||
+  if (!encode_tmap_u8(&ta, g.A, g.M, g.K, 128) || !encode_tmap_u8(&tw, g.W, g.N, g.K, 64) ||
       !encode_tmap_out(&tc, g.C, BF16 ? 2 : 4, g.M, g.N, g.N))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> attr{0};
@@ -314,9 +315,101 @@ cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
   return launch_pdl(gemm_f8_pair_kernel<BF16>, dim3(2 * pairs), dim3(THREADS), SMEM, st, ta, tw, tc, a);
 }
 
+// ------------------------------------------------------------------ few rows
+// Up to 32 rows of A: bound by reading W once, so the weights are the M side of mma.sync
+// (16 of them a CTA) and the rows of A its columns, eight to an MMA.  A CTA's sixteen warps
+// take the k blocks in turn, each with its own sum; the sums are added in shared memory in a
+// fixed order.  Operands come straight from global memory in 16-byte pieces: the sum runs
+// over k in any order, so a thread's sixteen consecutive bytes fill its k slots of two MMAs.
+template <int NT>
+constexpr int few_warps = NT <= 2 ? 16 : 8;
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: groups of eight rows of A
+template <int NT, bool BF16>
+__global__ void __launch_bounds__(32 * few_warps<NT>, 1) gemm_f8_few_kernel(const F8Gemm p) {
+  constexpr int FEW_WARPS = few_warps<NT>;
+  __shared__ float s_sum[FEW_WARPS][16][8 * NT + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int n0 = blockIdx.x * 16, kblocks = (p.K + kF8Group - 1) / kF8Group, nblocks = (p.N + kF8Group - 1) / kF8Group;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  grid_dependency_sync();
+  float acc[NT][4] = {};
+#pragma unroll(NT == 1 ? 2 : 1)
+  for (int kb = warp; kb < kblocks; kb += FEW_WARPS) {
+    uint4 w[2][2], x[NT][2];
+    float sa[NT][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = kb * kF8Group + 16 * c + 64 * u;
+      const bool in = k < p.K;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        w[r][u] = in ? __ldg(reinterpret_cast<const uint4*>(p.W + (int64_t)(n0 + g + 8 * r) * p.K + k)) : zero;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        x[t][u] = in && 8 * t + g < p.M ? __ldg(reinterpret_cast<const uint4*>(p.A + (int64_t)(8 * t + g) * p.K + k))
+                                        : zero;
+    }
+    const float sw = __ldg(p.w_scales + (int64_t)kb * nblocks + n0 / kF8Group);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        sa[t][e] = 8 * t + 2 * c + e < p.M ? __ldg(p.a_scales + (int64_t)kb * p.M + 8 * t + 2 * c + e) : 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        mma_e4m3(d, w[0][u].x, w[1][u].x, w[0][u].y, w[1][u].y, x[t][u].x, x[t][u].y);
+        mma_e4m3(d, w[0][u].z, w[1][u].z, w[0][u].w, w[1][u].w, x[t][u].z, x[t][u].w);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(sa[t][e & 1] * sw, d[e], acc[t][e]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s_sum[warp][g + 4 * (e & 2)][8 * t + 2 * c + (e & 1)] = acc[t][e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * 8 * NT; i += 32 * FEW_WARPS) {
+    const int n = i & 15, m = i >> 4;
+    float y = 0.f;
+#pragma unroll
+    for (int k = 0; k < FEW_WARPS; ++k) y += s_sum[k][n][m];
+    if (m < p.M) {
+      if (p.bias) y += __ldg(p.bias + n0 + n);
+      if (BF16)
+        static_cast<__nv_bfloat16*>(p.C)[(int64_t)m * p.N + n0 + n] = __float2bfloat16_rn(y);
+      else
+        static_cast<float*>(p.C)[(int64_t)m * p.N + n0 + n] = y;
+    }
+  }
+}
+
+template <int NT>
+cudaError_t launch_few(const F8Gemm& g, cudaStream_t st) {
+  return launch_pdl(g.bf16 ? gemm_f8_few_kernel<NT, true> : gemm_f8_few_kernel<NT, false>, dim3(g.N / 16),
+                    dim3(32 * few_warps<NT>), 0, st, g);
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_f8(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
+  // 4608 x 1536, us: 1 row 3.4 (CTA pairs 9.3), 8 rows 3.9 (8.5), 16 rows 5.1 (8.1), 32 rows
+  // 7.7 (8.0); 1536 x 4096: 16 rows 4.3 (12.6), 32 rows 7.0 (12.7)
+  if (g.M <= 8) return launch_few<1>(g, st);
+  if (g.M <= 16) return launch_few<2>(g, st);
+  if (g.M <= 32) return launch_few<4>(g, st);
   return g.bf16 ? launch_pair<true>(g, err, sms, st) : launch_pair<false>(g, err, sms, st);
 }
 

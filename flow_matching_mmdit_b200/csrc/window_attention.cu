@@ -297,14 +297,18 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, cudaSt
 // operand, eight softmax warps a tile hold the running maximum and sum, and O_X is
 // rescaled only when a row's maximum grows by more than 2^8.
 //   warps 0..15 softmax (X = warp / 8);  16 TMA;  17 S issuer;  18 P V issuer
+//   warp 19 zeroes V rows
 // Key tiles of 128 that no row of the CTA attends are never read: the walk goes through
-// the tiles of the sinks and then those of the window.  A tile inside every row's range
-// takes no mask; in the others each score is compared with its row's range.
+// the tiles of the sinks and then those of the window, and each query tile takes part in
+// those that its own rows attend.  A key tile inside every row's range takes no mask; in
+// the others a thread turns its rows' ranges into one bit per score.
+// V rows of keys that no row of the CTA attends (padding, evicted tokens) become zeros in
+// shared memory: their weights are zero, but zero times what they hold need not be.
 // TMEM columns: S_0 [0,128), S_1 [128,256), O_0 [256,320), O_1 [320,384), P_0 [384,448),
 // P_1 [448,512).
 namespace tc {
 
-constexpr int BQ = 128, BKV = 128, STAGES = 3, THREADS = 608;
+constexpr int BQ = 128, BKV = 128, STAGES = 3, THREADS = 640;
 constexpr uint32_t Q_BYTES = BQ * 64 * 2, KV_BYTES = BKV * 64 * 2;
 constexpr uint32_t OFF_KV = 2 * Q_BYTES, OFF_BAR = OFF_KV + STAGES * 2 * KV_BYTES;
 constexpr size_t SMEM = 1024 + OFF_BAR + 256;
@@ -317,11 +321,59 @@ struct Bars {
   uint64_t s_free[2];    // softmax -> MMA: S_X read into registers
   uint64_t p_full[2];    // softmax -> MMA: P_X written, O_X rescaled
   uint64_t pv_done[2];   // MMA -> softmax: O_X += P_X V finished
+  uint64_t v_clean[STAGES];   // V rows that nobody attends are zero (key tiles that have any)
   uint64_t stagger;      // tile 0 -> tile 1: tile 0 finished its first exponentials
   uint64_t drain[2];     // each MMA issuer's own completion after an abort
   uint32_t tmem_slot;
 };
 static_assert(sizeof(Bars) <= 256, "barriers overflow their shared-memory reserve");
+
+// The CTA's walk over key tiles: j = 0 .. count-1 are the tiles [0, sinks) and then first,
+// first + 1, ...; query tile x takes part in the sinks' tiles and in j of [begin[x], end[x]).
+struct Walk {
+  int count, sinks, first;
+  int sink, lo, hi;            // keys any row attends: [0, sink) and [lo, hi)
+  int begin[2], end[2];
+  __device__ __forceinline__ int key(int j) const { return (j < sinks ? j : first + (j - sinks)) * BKV; }
+  __device__ __forceinline__ bool takes(int x, int j) const { return j < sinks || (j >= begin[x] && j < end[x]); }
+  // whether the tile holds keys that no row of the CTA attends
+  __device__ __forceinline__ bool dirty(int j) const {
+    const int k = key(j);
+    return k + BKV > hi || (k < lo && k + BKV > sink);
+  }
+};
+__device__ __forceinline__ Walk walk_of(const WindowArgs& a, int start, int len, int q0, int tiles) {
+  Walk w;
+  const KeyRange first = key_range(a, start + q0, len);
+  const KeyRange last = key_range(a, start + min(q0 + 2 * BQ, a.n_q) - 1, len);
+  w.hi = last.hi;
+  w.lo = min(first.lo, w.hi);
+  w.sink = min(last.s, w.lo);
+  w.first = w.lo / BKV;
+  const int window = w.hi > w.lo ? (w.hi + BKV - 1) / BKV - w.first : 0;
+  w.sinks = (w.sink + BKV - 1) / BKV;
+  if (window > 0) w.sinks = min(w.sinks, w.first);
+  w.count = w.sinks + window;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    // rows of query tile x (the first tile's, when the second holds none)
+    const int r0 = q0 + (x < tiles ? x : 0) * BQ, r1 = min(r0 + BQ, a.n_q) - 1;
+    const KeyRange z = key_range(a, start + r1, len);
+    const int lo = key_range(a, start + r0, len).lo;
+    // sinks that reach into the window's tiles are met there, from the first one on
+    w.begin[x] = w.sinks + (z.s > w.sinks * BKV ? 0 : max(min(lo, w.hi) / BKV - w.first, 0));
+    w.end[x] = min(w.sinks + (z.hi + BKV - 1) / BKV - w.first, w.count);
+  }
+  return w;
+}
+
+// Bit i (key 8 (i / 2) + i % 2 of a thread's share) set where the key is below t.
+__device__ __forceinline__ uint32_t below(int t) {
+  if (t <= 0) return 0u;
+  if (t >= BKV) return ~0u;
+  const int n = 2 * (t >> 3) + min(t & 7, 2);
+  return n >= 32 ? ~0u : (1u << n) - 1u;
+}
 
 __global__ void __launch_bounds__(THREADS, 1)
     window_attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -337,27 +389,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int b = blockIdx.z, h = blockIdx.y, q0 = blockIdx.x * 2 * BQ;
   const int start = spans.start[b], len = spans.len[b];
   const int tiles = a.n_q - q0 > BQ ? 2 : 1;          // the second tile may hold no row
-  // key tiles: [0, sink_tiles), then first_tile, first_tile + 1, ... nkv of them in all
-  // that hold the keys any row of the CTA attends, [0, sink) and [lo, hi)
-  int nkv, sink_tiles, first_tile, sink, lo, hi;
-  {
-    const KeyRange first = key_range(a, start + q0, len);
-    const KeyRange last = key_range(a, start + min(q0 + 2 * BQ, a.n_q) - 1, len);
-    hi = last.hi;
-    lo = min(first.lo, hi);
-    sink = min(last.s, lo);
-    first_tile = lo / BKV;
-    const int window_tiles = hi > lo ? (hi + BKV - 1) / BKV - first_tile : 0;
-    sink_tiles = (sink + BKV - 1) / BKV;
-    if (window_tiles > 0) sink_tiles = min(sink_tiles, first_tile);
-    nkv = sink_tiles + window_tiles;
-  }
+  const Walk walk = walk_of(a, start, len, q0, tiles);
+  const int nkv = walk.count;
 
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 1);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&bar.kv_full[s], 1);
-      mbar_init(&bar.kv_empty[s], 2);
+      mbar_init(&bar.kv_empty[s], 3);
+      mbar_init(&bar.v_clean[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar.s_full[x], 1);
@@ -395,14 +435,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = 0; j < nkv; ++j) {
         const int s = j % STAGES;
         const uint32_t ph = (j / STAGES) & 1;
-        const int kt = j < sink_tiles ? j : first_tile + (j - sink_tiles);
         if (!mbar_wait(&bar.kv_empty[s], ph ^ 1, err)) {
           ok = false;
           break;
         }
         mbar_expect_tx(&bar.kv_full[s], 2 * KV_BYTES);
-        tma_load_3d(sKV + s * 2 * KV_BYTES, &tmK, &bar.kv_full[s], 0, kt * BKV, bhk);
-        tma_load_3d(sKV + s * 2 * KV_BYTES + KV_BYTES, &tmV, &bar.kv_full[s], 0, kt * BKV, bhk);
+        tma_load_3d(sKV + s * 2 * KV_BYTES, &tmK, &bar.kv_full[s], 0, walk.key(j), bhk);
+        tma_load_3d(sKV + s * 2 * KV_BYTES + KV_BYTES, &tmV, &bar.kv_full[s], 0, walk.key(j), bhk);
         issued[s] = true;
         last_parity[s] = ph;
       }
@@ -417,6 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------------------------------------------------------- S issuer
     if (lane == 0 && nkv > 0) {
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, BKV);
+      int n0 = 0, n1 = 0;
       bool ok = mbar_wait(&bar.q_full, 0, err);
       tc_fence_after();
       for (int j = 0; ok && j < nkv; ++j) {
@@ -425,7 +465,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         const uint64_t kdesc = umma_desc_sw128(smem_u32(sKV + s * 2 * KV_BYTES));
         for (int x = 0; x < tiles; ++x) {
-          if (j > 0 && !mbar_wait(&bar.s_free[x], (j - 1) & 1, err)) {
+          if (!walk.takes(x, j)) continue;
+          const int n = x ? n1++ : n0++;          // key tiles this query tile has had before
+          if (n > 0 && !mbar_wait(&bar.s_free[x], (n - 1) & 1, err)) {
             ok = false;
             break;
           }
@@ -447,11 +489,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_pv = umma_idesc_bf16_bmn(128, 64);
       bool ok = true;
+      int n0 = 0, n1 = 0;
+      uint32_t cleaned = 0;                       // bit s: parity of stage s's next v_clean
       for (int j = 0; ok && j < nkv; ++j) {
         const int s = j % STAGES;
         const uint32_t vbase = smem_u32(sKV + s * 2 * KV_BYTES + KV_BYTES);
+        if (walk.dirty(j)) {
+          ok = mbar_wait(&bar.v_clean[s], (cleaned >> s) & 1, err);
+          if (!ok) break;
+          cleaned ^= 1u << s;
+        }
         for (int x = 0; x < tiles; ++x) {
-          if (!mbar_wait(&bar.p_full[x], j & 1, err)) {
+          if (!walk.takes(x, j)) continue;
+          const int n = x ? n1++ : n0++;
+          if (!mbar_wait(&bar.p_full[x], n & 1, err)) {
             ok = false;
             break;
           }
@@ -460,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int k = 0; k < 8; ++k) {
             const uint64_t vdesc = umma_desc_sw128_mn(vbase + k * 2048);
             umma_bf16_ts(tmem + 256 + x * 64, tmem + 384 + x * 64 + 8 * k, vdesc, idesc_pv,
-                         (j > 0 || k > 0) ? 1u : 0u);
+                         (n > 0 || k > 0) ? 1u : 0u);
           }
           umma_commit(&bar.pv_done[x]);
         }
@@ -470,6 +521,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) umma_drain(&bar.drain[1]);   // no P V MMA still runs when TMEM is freed
     }
     __syncwarp();
+  } else if (warp == 19) {
+    // ---------------------------------------------------------------- V rows nobody attends
+    // every tile is waited for and released in turn, so that a stage's phases cannot be mistaken
+    for (int j = 0; j < nkv; ++j) {
+      const int s = j % STAGES, key0 = walk.key(j);
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / STAGES) & 1, err))) break;
+      if (walk.dirty(j)) {
+        uint4* v = reinterpret_cast<uint4*>(sKV + s * 2 * KV_BYTES + KV_BYTES);
+        for (int i = lane; i < BKV * 8; i += 32) {
+          const int key = key0 + (i >> 3);
+          if (key >= walk.hi || (key < walk.lo && key >= walk.sink)) v[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_clean[s]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.kv_empty[s]);
+    }
   } else if ((warp >> 3) < tiles) {
     // ---------------------------------------------------------------- softmax
     // Warp (quarter, half) of tile X reads TMEM lanes quarter*32 + half*16 + [0, 16); each
@@ -486,9 +556,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int all_s = ka.s, all_lo = kz.lo, all_hi = ka.hi;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     bool ok = true;
+    // this tile's n key tiles: the sinks' and those of its own part of the window
+    const int nx = walk.sinks + max(walk.end[x] - walk.begin[x], 0), skip = walk.begin[x] - walk.sinks;
+    const bool staggered = walk.sinks + walk.end[0] - walk.begin[0] > 0;    // tile 0 has key tiles
 #pragma unroll 2
-    for (int j = 0; j < nkv; ++j) {
-      const int key0 = (j < sink_tiles ? j : first_tile + (j - sink_tiles)) * BKV;
+    for (int j = 0; j < nx; ++j) {
+      const int key0 = (j < walk.sinks ? j : walk.first + skip + (j - walk.sinks)) * BKV;
       if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[x], j & 1, err))) {
         ok = false;
         break;
@@ -501,14 +574,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_free[x]);
       if (!(key0 + BKV <= all_s || (key0 >= all_lo && key0 + BKV <= all_hi))) {
+        const int base = key0 + cq;
+        const uint32_t on0 = below(k0.hi - base) & (~below(k0.lo - base) | below(k0.s - base));
+        const uint32_t on1 = below(k1.hi - base) & (~below(k1.lo - base) | below(k1.s - base));
 #pragma unroll
-        for (int g = 0; g < 16; ++g)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int key = key0 + 8 * g + cq + e;
-            if (key >= k0.hi || (key < k0.lo && key >= k0.s)) sc[4 * g + e] = -INFINITY;
-            if (key >= k1.hi || (key < k1.lo && key >= k1.s)) sc[4 * g + 2 + e] = -INFINITY;
-          }
+        for (int i = 0; i < 32; ++i) {
+          if (!(on0 & (1u << i))) sc[4 * (i / 2) + i % 2] = -INFINITY;
+          if (!(on1 & (1u << i))) sc[4 * (i / 2) + 2 + i % 2] = -INFINITY;
+        }
       }
       float p0[4], p1[4];
 #pragma unroll
@@ -539,7 +612,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t sl2 = f2_pack(a.scale_log2, a.scale_log2);
       const float n0 = m0 == -INFINITY ? 0.f : -m0, n1 = m1 == -INFINITY ? 0.f : -m1;
       const uint64_t nb0 = f2_pack(n0, n0), nb1 = f2_pack(n1, n1);
-      if (x == 1 && j == 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.stagger, 0, err))) {
+      if (x == 1 && j == 0 && staggered && !__all_sync(0xffffffffu, mbar_wait(&bar.stagger, 0, err))) {
         ok = false;
         break;
       }
@@ -576,22 +649,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_after();
       }
-      // V rows of keys that no row of the CTA attends (padding, evicted tokens) become zeros:
-      // their weights are zero, but zero times what they hold need not be.  Tile 0's warps do
-      // it before they release P_0, and both tiles' P V follow that.
-      if (x == 0 && (key0 + BKV > hi || (key0 < lo && key0 + BKV > sink))) {
-        const int s = j % STAGES;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / STAGES) & 1, err))) {
-          ok = false;
-          break;
-        }
-        uint4* v = reinterpret_cast<uint4*>(sKV + s * 2 * KV_BYTES + KV_BYTES);
-        for (int i = threadIdx.x; i < BKV * 8; i += 256) {
-          const int key = key0 + (i >> 3);
-          if (key >= hi || (key < lo && key >= sink)) v[i] = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-      }
       tmem_st_16x128b_x16(lane_addr + p_col, pk);
       if (j > 0 && __any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
         float o[32];
@@ -616,9 +673,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (__all_sync(0xffffffffu, ok && (nkv == 0 || mbar_wait(&bar.pv_done[x], (nkv - 1) & 1, err)))) {
+    if (__all_sync(0xffffffffu, ok && (nx == 0 || mbar_wait(&bar.pv_done[x], (nx - 1) & 1, err)))) {
       float o[32];
-      if (nkv > 0) {
+      if (nx > 0) {
         tc_fence_after();
         tmem_ld_16x256b_x8(lane_addr + o_col, o);
         tmem_ld_wait();
