@@ -79,14 +79,14 @@ __device__ __forceinline__ void attend_row(const WindowArgs& a, int b, int h, in
 // 16, by mma.sync: a tile of the tensor cores' 128 rows would be mostly padding, and
 // the work is reading K and V once.  The keys that any row of the tile attends are cut
 // into steps of 32 that the warps of a cluster of CTAs take in turn, each with its own
-// running softmax; the CTAs' partial results are joined through distributed shared
-// memory, so one launch does it all.
+// running softmax; each CTA finishes a share of the rows from the parts that the others
+// write into its shared memory, so one launch does it all.
 // Operands come straight from global memory in 16-byte pieces, without shared memory:
 // both products sum over, or run along, an index whose order is free.  For S = Q K^T the
 // 64 columns are dealt to the MMA's k slots so that a thread's eight consecutive columns
 // fill its slots of two steps; for O = P V output column n of MMA j is column 8 n + j, so
 // that a thread's eight consecutive columns of a V row feed the eight MMAs.
-constexpr int kFewWarps = 4, kFewStep = 32, kFewMaxSplit = 8;
+constexpr int kFewStep = 32, kFewMaxSplit = 8;
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -94,21 +94,25 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "f"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__global__ void __launch_bounds__(32 * kFewWarps) window_attention_few_kernel(const WindowArgs a,
-                                                                              const RowSpans spans, int splits) {
-  __shared__ float s_o[kFewWarps][16][66];    // partial O of each warp, then of the CTA in [0]
-  __shared__ float s_m[kFewWarps][16], s_l[kFewWarps][16];
+template <int SPLITS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
+    window_attention_few_kernel(const __grid_constant__ WindowArgs a, const __grid_constant__ RowSpans spans) {
+  constexpr int splits = SPLITS, share = 16 / splits;     // rows that a CTA finishes
+  __shared__ float s_o[WARPS][16][66];                // O, maximum and sum of each warp
+  __shared__ float s_m[WARPS][16], s_l[WARPS][16];
+  __shared__ float s_part[splits][share][66];             // of each CTA: O, then maximum and sum
   __shared__ int s_redo[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int rank = blockIdx.x % splits, tile = blockIdx.x / splits, hk = blockIdx.y, b = blockIdx.z;
   const int group = a.heads / a.kv_heads, rows = a.n_q * group, row0 = tile * 16;
   const int start = spans.start[b], len = spans.len[b];
+  if constexpr (splits > 1) cluster_arrive();             // waited for before the others are written to
   grid_dependency_sync();
 
   // this thread's rows g and g + 8 (a row past the last repeats it and is not stored)
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) window_attention_few_kernel(co
   const uint4 *kp = reinterpret_cast<const uint4*>(a.k + ((int64_t)b * a.kv_heads + hk) * a.n_kv * 64),
               *vp = reinterpret_cast<const uint4*>(a.v + ((int64_t)b * a.kv_heads + hk) * a.n_kv * 64);
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, o[8][4] = {};
-  for (int at = (rank * kFewWarps + warp) * kFewStep; at < count; at += splits * kFewWarps * kFewStep) {
+  for (int at = (rank * WARPS + warp) * kFewStep; at < count; at += splits * WARPS * kFewStep) {
     uint4 kr[4][2], vr[2][4];
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -232,36 +236,73 @@ __global__ void __launch_bounds__(32 * kFewWarps) window_attention_few_kernel(co
     s_o[warp][g + 8][16 * c + 8 + j] = o[j][3];
   }
   if (threadIdx.x < 16) s_redo[threadIdx.x] = 0;
-  cluster_sync_all();
-  // every CTA finishes its share of the rows from all CTAs' warps, in a fixed order
-  const int share = 16 / splits;                  // splits is a power of two up to 8
-  for (int e = threadIdx.x; e < share * 64; e += blockDim.x) {
-    const int r = rank * share + (e >> 6), d = e & 63;
-    float m = -INFINITY;
-    for (int k = 0; k < splits; ++k)
+  __syncthreads();
+  if constexpr (splits > 1) cluster_wait();
+  for (int e = threadIdx.x; e < 16 * 64; e += 32 * WARPS) {
+    const int r = e >> 6, d = e & 63;
+    float m = s_m[0][r];
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) m = fmaxf(m, ld_cluster(&s_m[w][r], k));
+    for (int w = 1; w < WARPS; ++w) m = fmaxf(m, s_m[w][r]);
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f, x = 0.f;
-    for (int k = 0; k < splits; ++k)
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
-        const float f = ex2(ld_cluster(&s_m[w][r], k) - base);
-        l += f * ld_cluster(&s_l[w][r], k);
-        x += f * ld_cluster(&s_o[w][r][d], k);
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = ex2(s_m[w][r] - base);
+      l += f * s_l[w][r];
+      x += f * s_o[w][r][d];
+    }
+    float* part = s_part[rank][r % share];
+    if constexpr (splits > 1) {
+      st_cluster(part + d, r / share, x);
+      if (d == 0) {
+        st_cluster(part + 64, r / share, m);
+        st_cluster(part + 65, r / share, l);
       }
+    } else {
+      part[d] = x;
+      if (d == 0) part[64] = m, part[65] = l;
+    }
+  }
+  if constexpr (splits > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  // every CTA finishes its share of the rows from all CTAs' parts, in a fixed order
+  for (int e = threadIdx.x; e < share * 64; e += 32 * WARPS) {
+    const int r = rank * share + (e >> 6), d = e & 63;
+    float m[splits], l[splits], x[splits];
+#pragma unroll
+    for (int k = 0; k < splits; ++k) {
+      const float* part = s_part[k][e >> 6];
+      x[k] = part[d];
+      m[k] = part[64];
+      l[k] = part[65];
+    }
+    float top = m[0];
+#pragma unroll
+    for (int k = 1; k < splits; ++k) top = fmaxf(top, m[k]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, y = 0.f;
+#pragma unroll
+    for (int k = 0; k < splits; ++k) {
+      const float f = ex2(m[k] - base);
+      sum += f * l[k];
+      y += f * x[k];
+    }
     // a row with no attended key (or only scores of -inf) writes zeros
-    const float y = l == 0.f ? 0.f : x / l;
+    y = sum == 0.f ? 0.f : y / sum;
     if (row0 + r < rows) {
       const int i = (row0 + r) / group, h = hk * group + (row0 + r) % group;
       a.out[(((int64_t)b * a.n_q + i) * a.heads + h) * 64 + d] = __float2bfloat16_rn(y);
       if (!isfinite(y)) s_redo[r] = 1;
     }
   }
-  cluster_sync_all();                             // no CTA leaves while its partials may be read
+  __syncthreads();
   // A non-finite value in V reaches the whole tile through a weight of zero: rows that came
   // out non-finite are done again from their attended keys alone.
-  for (int r = rank * share + warp; r < (rank + 1) * share; r += kFewWarps)
+  for (int r = rank * share + warp; r < (rank + 1) * share; r += WARPS)
     if (s_redo[r])
       attend_row(a, b, hk * group + (row0 + r) % group, (row0 + r) / group, start + (row0 + r) / group, len);
 }
@@ -273,10 +314,13 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, cudaSt
   const int64_t most = (int64_t)a.left + a.right + 16 + a.sinks;
   const int64_t keys = most < a.n_kv ? most : a.n_kv;
   int splits = 1;
-  while (splits < kFewMaxSplit && splits * kFewWarps * kFewStep < keys) splits *= 2;
+  while (splits < kFewMaxSplit && splits * 4 * kFewStep < keys) splits *= 2;
+  // past two steps a warp: eight warps a CTA (8192 keys, 32 heads on 8: 10.2 us for 15.5;
+  // 1028 keys: 15.5 for 8.0, fewer CTAs fit an SM)
+  const bool wide = splits == kFewMaxSplit && keys > 2 * kFewMaxSplit * 4 * kFewStep;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((rows + 15) / 16 * splits, a.kv_heads, B);
-  cfg.blockDim = dim3(32 * kFewWarps);
+  cfg.blockDim = dim3(wide ? 256 : 128);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -287,65 +331,68 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, cudaSt
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, window_attention_few_kernel, a, spans, splits);
+  if (wide) return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<8, 8>, a, spans);
+  switch (splits) {
+    case 1: return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<1, 4>, a, spans);
+    case 2: return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<2, 4>, a, spans);
+    case 4: return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<4, 4>, a, spans);
+    default: return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<8, 4>, a, spans);
+  }
 }
 
 // ------------------------------------------------------------------ many rows
-// One CTA per (256 query rows = two 128-row tiles X = 0, 1; head; batch row) on the tcgen05
-// tensor cores, with the roles of the joint-attention kernel (attention.cu): S_X = Q_X K^T
-// and O_X += P_X V accumulate in TMEM, P_X goes back to TMEM as the second product's A
-// operand, eight softmax warps a tile hold the running maximum and sum, and O_X is
-// rescaled only when a row's maximum grows by more than 2^8.
-//   warps 0..15 softmax (X = warp / 8);  16 TMA;  17 S issuer;  18 P V issuer
-//   warp 19 zeroes V rows
+// One CTA per (128 query rows, head, batch row) on the tcgen05 tensor cores, two to an SM.
+// As in the joint-attention kernel (attention.cu) S = Q K^T and O += P V accumulate in
+// TMEM, P goes back to TMEM as the second product's A operand, eight softmax warps hold
+// the running maximum and sum, and O is rescaled only when a row's maximum grows by more
+// than 2^8.  There one CTA holds two query tiles that take turns on the exponential unit;
+// here the two are CTAs of their own, which also hides one's start and end behind the other
+// (a window is only a few key tiles long) and lets each walk its own keys.
+//   warp 0 TMA;  1 S issuer;  2 P V issuer;  3 zeroes V rows;  4..11 softmax
 // Key tiles of 128 that no row of the CTA attends are never read: the walk goes through
-// the tiles of the sinks and then those of the window, and each query tile takes part in
-// those that its own rows attend.  A key tile inside every row's range takes no mask; in
-// the others a thread turns its rows' ranges into one bit per score.
+// the tiles of the sinks and then those of the window.  A key tile inside every row's
+// range takes no mask; in the others a thread turns its rows' ranges into one bit per score.
 // V rows of keys that no row of the CTA attends (padding, evicted tokens) become zeros in
 // shared memory: their weights are zero, but zero times what they hold need not be.
-// TMEM columns: S_0 [0,128), S_1 [128,256), O_0 [256,320), O_1 [320,384), P_0 [384,448),
-// P_1 [448,512).
+// TMEM columns: S [0, 128), O [128, 192), P [192, 256).
 namespace tc {
 
-constexpr int BQ = 128, BKV = 128, STAGES = 3, THREADS = 640;
+constexpr int BQ = 128, BKV = 128, STAGES = 3, THREADS = 384;
 constexpr uint32_t Q_BYTES = BQ * 64 * 2, KV_BYTES = BKV * 64 * 2;
-constexpr uint32_t OFF_KV = 2 * Q_BYTES, OFF_BAR = OFF_KV + STAGES * 2 * KV_BYTES;
-constexpr size_t SMEM = 1024 + OFF_BAR + 256;
+constexpr uint32_t OFF_KV = Q_BYTES, OFF_BAR = OFF_KV + STAGES * 2 * KV_BYTES;
+constexpr size_t SMEM = OFF_BAR + 256;             // two CTAs share an SM's 228 KB
+constexpr uint32_t O_COL = 128, P_COL = 192;
 constexpr float kRescaleThreshold = 8.0f;          // log2 units
 
 struct Bars {
   uint64_t q_full;
   uint64_t kv_full[STAGES], kv_empty[STAGES];
-  uint64_t s_full[2];    // MMA -> softmax: S_X ready
-  uint64_t s_free[2];    // softmax -> MMA: S_X read into registers
-  uint64_t p_full[2];    // softmax -> MMA: P_X written, O_X rescaled
-  uint64_t pv_done[2];   // MMA -> softmax: O_X += P_X V finished
   uint64_t v_clean[STAGES];   // V rows that nobody attends are zero (key tiles that have any)
-  uint64_t stagger;      // tile 0 -> tile 1: tile 0 finished its first exponentials
+  uint64_t s_full;       // MMA -> softmax: S ready
+  uint64_t s_free;       // softmax -> MMA: S read into registers
+  uint64_t p_full;       // softmax -> MMA: P written, O rescaled
+  uint64_t pv_done;      // MMA -> softmax: O += P V finished
   uint64_t drain[2];     // each MMA issuer's own completion after an abort
   uint32_t tmem_slot;
 };
 static_assert(sizeof(Bars) <= 256, "barriers overflow their shared-memory reserve");
 
 // The CTA's walk over key tiles: j = 0 .. count-1 are the tiles [0, sinks) and then first,
-// first + 1, ...; query tile x takes part in the sinks' tiles and in j of [begin[x], end[x]).
+// first + 1, ...
 struct Walk {
   int count, sinks, first;
   int sink, lo, hi;            // keys any row attends: [0, sink) and [lo, hi)
-  int begin[2], end[2];
   __device__ __forceinline__ int key(int j) const { return (j < sinks ? j : first + (j - sinks)) * BKV; }
-  __device__ __forceinline__ bool takes(int x, int j) const { return j < sinks || (j >= begin[x] && j < end[x]); }
   // whether the tile holds keys that no row of the CTA attends
   __device__ __forceinline__ bool dirty(int j) const {
     const int k = key(j);
     return k + BKV > hi || (k < lo && k + BKV > sink);
   }
 };
-__device__ __forceinline__ Walk walk_of(const WindowArgs& a, int start, int len, int q0, int tiles) {
+__device__ __forceinline__ Walk walk_of(const WindowArgs& a, int start, int len, int q0) {
   Walk w;
   const KeyRange first = key_range(a, start + q0, len);
-  const KeyRange last = key_range(a, start + min(q0 + 2 * BQ, a.n_q) - 1, len);
+  const KeyRange last = key_range(a, start + min(q0 + BQ, a.n_q) - 1, len);
   w.hi = last.hi;
   w.lo = min(first.lo, w.hi);
   w.sink = min(last.s, w.lo);
@@ -354,16 +401,6 @@ __device__ __forceinline__ Walk walk_of(const WindowArgs& a, int start, int len,
   w.sinks = (w.sink + BKV - 1) / BKV;
   if (window > 0) w.sinks = min(w.sinks, w.first);
   w.count = w.sinks + window;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    // rows of query tile x (the first tile's, when the second holds none)
-    const int r0 = q0 + (x < tiles ? x : 0) * BQ, r1 = min(r0 + BQ, a.n_q) - 1;
-    const KeyRange z = key_range(a, start + r1, len);
-    const int lo = key_range(a, start + r0, len).lo;
-    // sinks that reach into the window's tiles are met there, from the first one on
-    w.begin[x] = w.sinks + (z.s > w.sinks * BKV ? 0 : max(min(lo, w.hi) / BKV - w.first, 0));
-    w.end[x] = min(w.sinks + (z.hi + BKV - 1) / BKV - w.first, w.count);
-  }
   return w;
 }
 
@@ -375,21 +412,23 @@ __device__ __forceinline__ uint32_t below(int t) {
   return n >= 32 ? ~0u : (1u << n) - 1u;
 }
 
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 2)
     window_attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WindowArgs a,
                                const __grid_constant__ RowSpans spans, int* err) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = sm;
+  extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* sKV = sm + OFF_KV;
   Bars& bar = *reinterpret_cast<Bars*>(sm + OFF_BAR);
+  // 128-byte swizzled tiles need this alignment, and there is no room left to round up
+  if (smem_u32(sm) & 1023) {
+    if (threadIdx.x == 0) atomicCAS(err, 0, 1);
+    return;
+  }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.z, h = blockIdx.y, q0 = blockIdx.x * 2 * BQ;
+  const int b = blockIdx.z, h = blockIdx.y, q0 = blockIdx.x * BQ;
   const int start = spans.start[b], len = spans.len[b];
-  const int tiles = a.n_q - q0 > BQ ? 2 : 1;          // the second tile may hold no row
-  const Walk walk = walk_of(a, start, len, q0, tiles);
+  const Walk walk = walk_of(a, start, len, q0);
   const int nkv = walk.count;
 
   if (threadIdx.x == 0) {
@@ -399,13 +438,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&bar.kv_empty[s], 3);
       mbar_init(&bar.v_clean[s], 1);
     }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&bar.s_full[x], 1);
-      mbar_init(&bar.s_free[x], 8);
-      mbar_init(&bar.p_full[x], 8);
-      mbar_init(&bar.pv_done[x], 1);
-    }
-    mbar_init(&bar.stagger, 8);
+    mbar_init(&bar.s_full, 1);
+    mbar_init(&bar.s_free, 8);
+    mbar_init(&bar.p_full, 8);
+    mbar_init(&bar.pv_done, 1);
     mbar_init(&bar.drain[0], 1);
     mbar_init(&bar.drain[1], 1);
     fence_mbar_init();
@@ -413,8 +449,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  if (warp == 17) {
-    tmem_alloc(&bar.tmem_slot, 512);
+  if (warp == 1) {
+    tmem_alloc(&bar.tmem_slot, 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -423,132 +459,113 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = bar.tmem_slot;
   grid_dependency_sync();    // set-up above touched only shared memory and TMEM
 
-  if (warp == 16) {
-    // ---------------------------------------------------------------- TMA producer
-    if (lane == 0 && nkv > 0) {
-      uint32_t last_parity[STAGES] = {0, 0, 0};
-      bool issued[STAGES] = {false, false, false};
-      bool ok = true;
-      const int bh = b * a.heads + h, bhk = b * a.kv_heads + h / (a.heads / a.kv_heads);
-      mbar_expect_tx(&bar.q_full, tiles * Q_BYTES);
-      for (int x = 0; x < tiles; ++x) tma_load_3d(sQ + x * Q_BYTES, &tmQ, &bar.q_full, 0, q0 + x * BQ, bh);
-      for (int j = 0; j < nkv; ++j) {
-        const int s = j % STAGES;
-        const uint32_t ph = (j / STAGES) & 1;
-        if (!mbar_wait(&bar.kv_empty[s], ph ^ 1, err)) {
-          ok = false;
-          break;
-        }
-        mbar_expect_tx(&bar.kv_full[s], 2 * KV_BYTES);
-        tma_load_3d(sKV + s * 2 * KV_BYTES, &tmK, &bar.kv_full[s], 0, walk.key(j), bhk);
-        tma_load_3d(sKV + s * 2 * KV_BYTES + KV_BYTES, &tmV, &bar.kv_full[s], 0, walk.key(j), bhk);
-        issued[s] = true;
-        last_parity[s] = ph;
-      }
-      mbar_wait_drain(&bar.q_full, 0);
-      // after an abort the consumers may not have waited for every stage filled here
-      if (!ok || err_raised(err))
-        for (int s = 0; s < STAGES; ++s)
-          if (issued[s]) mbar_wait_drain(&bar.kv_full[s], last_parity[s]);
-    }
-    __syncwarp();
-  } else if (warp == 17) {
-    // ---------------------------------------------------------------- S issuer
-    if (lane == 0 && nkv > 0) {
-      constexpr uint32_t idesc_s = umma_idesc_bf16(128, BKV);
-      int n0 = 0, n1 = 0;
-      bool ok = mbar_wait(&bar.q_full, 0, err);
-      tc_fence_after();
-      for (int j = 0; ok && j < nkv; ++j) {
-        const int s = j % STAGES;
-        ok = mbar_wait(&bar.kv_full[s], (j / STAGES) & 1, err);
-        if (!ok) break;
-        const uint64_t kdesc = umma_desc_sw128(smem_u32(sKV + s * 2 * KV_BYTES));
-        for (int x = 0; x < tiles; ++x) {
-          if (!walk.takes(x, j)) continue;
-          const int n = x ? n1++ : n0++;          // key tiles this query tile has had before
-          if (n > 0 && !mbar_wait(&bar.s_free[x], (n - 1) & 1, err)) {
+  // 64 scores a softmax thread do not fit an even share of the registers (80): its two
+  // warpgroups take over what the first gives up (32 + 2 x 104 = 3 x 80)
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    if (warp == 0) {
+      // -------------------------------------------------------------- TMA producer
+      if (lane == 0 && nkv > 0) {
+        int issued = 0;
+        bool ok = true;
+        const int bh = b * a.heads + h, bhk = b * a.kv_heads + h / (a.heads / a.kv_heads);
+        mbar_expect_tx(&bar.q_full, Q_BYTES);
+        tma_load_3d(sm, &tmQ, &bar.q_full, 0, q0, bh);
+        for (int j = 0; j < nkv; ++j) {
+          const int s = j % STAGES;
+          if (!mbar_wait(&bar.kv_empty[s], ((j / STAGES) & 1) ^ 1, err)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint64_t qdesc = umma_desc_sw128(smem_u32(sQ + x * Q_BYTES));
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_bf16(tmem + x * 128, qdesc + 2 * k, kdesc + 2 * k, idesc_s, k > 0 ? 1u : 0u);
-          umma_commit(&bar.s_full[x]);
+          mbar_expect_tx(&bar.kv_full[s], 2 * KV_BYTES);
+          tma_load_3d(sKV + s * 2 * KV_BYTES, &tmK, &bar.kv_full[s], 0, walk.key(j), bhk);
+          tma_load_3d(sKV + s * 2 * KV_BYTES + KV_BYTES, &tmV, &bar.kv_full[s], 0, walk.key(j), bhk);
+          issued = j + 1;
         }
-        if (!ok) break;
-        umma_commit(&bar.kv_empty[s]);
-      }
-      if (!ok) umma_drain(&bar.drain[0]);   // no S MMA still runs when TMEM is freed
-    }
-    __syncwarp();
-  } else if (warp == 18) {
-    // ---------------------------------------------------------------- P V issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_pv = umma_idesc_bf16_bmn(128, 64);
-      bool ok = true;
-      int n0 = 0, n1 = 0;
-      uint32_t cleaned = 0;                       // bit s: parity of stage s's next v_clean
-      for (int j = 0; ok && j < nkv; ++j) {
-        const int s = j % STAGES;
-        const uint32_t vbase = smem_u32(sKV + s * 2 * KV_BYTES + KV_BYTES);
-        if (walk.dirty(j)) {
-          ok = mbar_wait(&bar.v_clean[s], (cleaned >> s) & 1, err);
-          if (!ok) break;
-          cleaned ^= 1u << s;
-        }
-        for (int x = 0; x < tiles; ++x) {
-          if (!walk.takes(x, j)) continue;
-          const int n = x ? n1++ : n0++;
-          if (!mbar_wait(&bar.p_full[x], n & 1, err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint64_t vdesc = umma_desc_sw128_mn(vbase + k * 2048);
-            umma_bf16_ts(tmem + 256 + x * 64, tmem + 384 + x * 64 + 8 * k, vdesc, idesc_pv,
-                         (n > 0 || k > 0) ? 1u : 0u);
-          }
-          umma_commit(&bar.pv_done[x]);
-        }
-        if (!ok) break;
-        umma_commit(&bar.kv_empty[s]);
-      }
-      if (!ok) umma_drain(&bar.drain[1]);   // no P V MMA still runs when TMEM is freed
-    }
-    __syncwarp();
-  } else if (warp == 19) {
-    // ---------------------------------------------------------------- V rows nobody attends
-    // every tile is waited for and released in turn, so that a stage's phases cannot be mistaken
-    for (int j = 0; j < nkv; ++j) {
-      const int s = j % STAGES, key0 = walk.key(j);
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / STAGES) & 1, err))) break;
-      if (walk.dirty(j)) {
-        uint4* v = reinterpret_cast<uint4*>(sKV + s * 2 * KV_BYTES + KV_BYTES);
-        for (int i = lane; i < BKV * 8; i += 32) {
-          const int key = key0 + (i >> 3);
-          if (key >= walk.hi || (key < walk.lo && key >= walk.sink)) v[i] = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v_clean[s]);
+        mbar_wait_drain(&bar.q_full, 0);
+        // after an abort the consumers may not have waited for every stage filled here
+        if (!ok || err_raised(err))
+          for (int j = max(issued - STAGES, 0); j < issued; ++j)
+            mbar_wait_drain(&bar.kv_full[j % STAGES], (j / STAGES) & 1);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.kv_empty[s]);
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- S issuer
+      if (lane == 0 && nkv > 0) {
+        constexpr uint32_t idesc_s = umma_idesc_bf16(128, BKV);
+        bool ok = mbar_wait(&bar.q_full, 0, err);
+        const uint64_t qdesc = umma_desc_sw128(smem_u32(sm));
+        for (int j = 0; ok && j < nkv; ++j) {
+          const int s = j % STAGES;
+          ok = mbar_wait(&bar.kv_full[s], (j / STAGES) & 1, err) &&
+               (j == 0 || mbar_wait(&bar.s_free, (j - 1) & 1, err));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kdesc = umma_desc_sw128(smem_u32(sKV + s * 2 * KV_BYTES));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) umma_bf16(tmem, qdesc + 2 * k, kdesc + 2 * k, idesc_s, k > 0 ? 1u : 0u);
+          umma_commit(&bar.s_full);
+          umma_commit(&bar.kv_empty[s]);
+        }
+        if (!ok) umma_drain(&bar.drain[0]);   // no S MMA still runs when TMEM is freed
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // -------------------------------------------------------------- P V issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc_pv = umma_idesc_bf16_bmn(128, 64);
+        bool ok = true;
+        uint32_t cleaned = 0;                       // bit s: parity of stage s's next v_clean
+        for (int j = 0; ok && j < nkv; ++j) {
+          const int s = j % STAGES;
+          const uint32_t vbase = smem_u32(sKV + s * 2 * KV_BYTES + KV_BYTES);
+          if (walk.dirty(j)) {
+            ok = mbar_wait(&bar.v_clean[s], (cleaned >> s) & 1, err);
+            cleaned ^= 1u << s;
+          }
+          ok = ok && mbar_wait(&bar.p_full, j & 1, err);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_ts(tmem + O_COL, tmem + P_COL + 8 * k, umma_desc_sw128_mn(vbase + k * 2048), idesc_pv,
+                         (j > 0 || k > 0) ? 1u : 0u);
+          umma_commit(&bar.pv_done);
+          umma_commit(&bar.kv_empty[s]);
+        }
+        if (!ok) umma_drain(&bar.drain[1]);   // no P V MMA still runs when TMEM is freed
+      }
+      __syncwarp();
+    } else {
+      // -------------------------------------------------------------- V rows nobody attends
+      // every tile is waited for and released in turn, so that a stage's phases cannot be
+      // mistaken
+      for (int j = 0; j < nkv; ++j) {
+        const int s = j % STAGES, key0 = walk.key(j);
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / STAGES) & 1, err))) break;
+        if (walk.dirty(j)) {
+          uint4* v = reinterpret_cast<uint4*>(sKV + s * 2 * KV_BYTES + KV_BYTES);
+          for (int i = lane; i < BKV * 8; i += 32) {
+            const int key = key0 + (i >> 3);
+            if (key >= walk.hi || (key < walk.lo && key >= walk.sink)) v[i] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.v_clean[s]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.kv_empty[s]);
+      }
     }
-  } else if ((warp >> 3) < tiles) {
+  } else {
     // ---------------------------------------------------------------- softmax
-    // Warp (quarter, half) of tile X reads TMEM lanes quarter*32 + half*16 + [0, 16); each
-    // thread holds rows rlo and rlo + 8, 32 of the 128 keys of each (columns 8g + cq +
-    // {0, 1}); the four threads of a row combine maxima by shuffles.
-    const int x = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-    const int wrow = x * BQ + quarter * 32 + half * 16, rlo = wrow + (lane >> 2);
-    const uint32_t lane_addr = tmem + (uint32_t(quarter * 32 + half * 16) << 16);
-    const uint32_t s_col = x * 128, o_col = 256 + x * 64, p_col = 384 + x * 64;
+    // Warp (quarter, half) reads TMEM lanes quarter*32 + half*16 + [0, 16); each thread holds
+    // rows rlo and rlo + 8, 32 of the 128 keys of each (columns 8g + cq + {0, 1}); the four
+    // threads of a row combine maxima by shuffles.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int half = (warp >> 2) - 1, quarter = warp & 3;
+    const int wrow = quarter * 32 + half * 16, rlo = wrow + (lane >> 2);
+    const uint32_t lane_addr = tmem + (uint32_t(wrow) << 16);
     const int cq = 2 * (lane & 3);
     const KeyRange k0 = key_range(a, start + q0 + rlo, len), k1 = key_range(a, start + q0 + rlo + 8, len);
     // keys that all sixteen rows of the warp attend: below all_s, and from all_lo to all_hi
@@ -556,23 +573,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int all_s = ka.s, all_lo = kz.lo, all_hi = ka.hi;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     bool ok = true;
-    // this tile's n key tiles: the sinks' and those of its own part of the window
-    const int nx = walk.sinks + max(walk.end[x] - walk.begin[x], 0), skip = walk.begin[x] - walk.sinks;
-    const bool staggered = walk.sinks + walk.end[0] - walk.begin[0] > 0;    // tile 0 has key tiles
 #pragma unroll 2
-    for (int j = 0; j < nx; ++j) {
-      const int key0 = (j < walk.sinks ? j : walk.first + skip + (j - walk.sinks)) * BKV;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[x], j & 1, err))) {
+    for (int j = 0; j < nkv; ++j) {
+      const int key0 = walk.key(j);
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full, j & 1, err))) {
         ok = false;
         break;
       }
       tc_fence_after();
       float sc[64];
-      tmem_ld_16x256b_x16(lane_addr + s_col, sc);
+      tmem_ld_16x256b_x8(lane_addr, *reinterpret_cast<float(*)[32]>(&sc[0]));
+      tmem_ld_16x256b_x8(lane_addr + 64, *reinterpret_cast<float(*)[32]>(&sc[32]));
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.s_free[x]);
+      if (lane == 0) mbar_arrive(&bar.s_free);
       if (!(key0 + BKV <= all_s || (key0 >= all_lo && key0 + BKV <= all_hi))) {
         const int base = key0 + cq;
         const uint32_t on0 = below(k0.hi - base) & (~below(k0.lo - base) | below(k0.s - base));
@@ -612,10 +627,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t sl2 = f2_pack(a.scale_log2, a.scale_log2);
       const float n0 = m0 == -INFINITY ? 0.f : -m0, n1 = m1 == -INFINITY ? 0.f : -m1;
       const uint64_t nb0 = f2_pack(n0, n0), nb1 = f2_pack(n1, n1);
-      if (x == 1 && j == 0 && staggered && !__all_sync(0xffffffffu, mbar_wait(&bar.stagger, 0, err))) {
-        ok = false;
-        break;
-      }
       uint64_t a0[2] = {0ull, 0ull}, a1[2] = {0ull, 0ull};
       uint32_t pk[32];
 #pragma unroll
@@ -633,26 +644,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         pk[2 * g] = pack_bf16x2(e0, e1);
         pk[2 * g + 1] = pack_bf16x2(e2, e3);
       }
-      if (x == 0 && j == 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.stagger);
-      }
       float s0, s1, s2, s3;
       f2_unpack(f2_add(a0[0], a0[1]), s0, s1);
       f2_unpack(f2_add(a1[0], a1[1]), s2, s3);
       l0 = l0 * c0 + (s0 + s1);
       l1 = l1 * c1 + (s2 + s3);
       if (j > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bar.pv_done[x], (j - 1) & 1, err))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (j - 1) & 1, err))) {
           ok = false;
           break;
         }
         tc_fence_after();
       }
-      tmem_st_16x128b_x16(lane_addr + p_col, pk);
+      tmem_st_16x128b_x16(lane_addr + P_COL, pk);
       if (j > 0 && __any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
         float o[32];
-        tmem_ld_16x256b_x8(lane_addr + o_col, o);
+        tmem_ld_16x256b_x8(lane_addr + O_COL, o);
         tmem_ld_wait();
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
@@ -661,23 +668,23 @@ __global__ void __launch_bounds__(THREADS, 1)
           o[4 * g + 2] *= c1;
           o[4 * g + 3] *= c1;
         }
-        tmem_st_16x256b_x8(lane_addr + o_col, o);
+        tmem_st_16x256b_x8(lane_addr + O_COL, o);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[x]);
+      if (lane == 0) mbar_arrive(&bar.p_full);
     }
     // row sums: the four threads of a row hold disjoint keys
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (__all_sync(0xffffffffu, ok && (nx == 0 || mbar_wait(&bar.pv_done[x], (nx - 1) & 1, err)))) {
+    if (__all_sync(0xffffffffu, ok && (nkv == 0 || mbar_wait(&bar.pv_done, (nkv - 1) & 1, err)))) {
       float o[32];
-      if (nx > 0) {
+      if (nkv > 0) {
         tc_fence_after();
-        tmem_ld_16x256b_x8(lane_addr + o_col, o);
+        tmem_ld_16x256b_x8(lane_addr + O_COL, o);
         tmem_ld_wait();
       } else {
 #pragma unroll
@@ -716,9 +723,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -735,12 +742,19 @@ cudaError_t launch_many(const WindowArgs& a, const RowSpans& spans, int B, int* 
   static std::atomic<uint64_t> attr{0};
   const cudaError_t e = ensure_smem_limit(tc::window_attention_tc_kernel, (int)tc::SMEM, attr);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tc::window_attention_tc_kernel, dim3((a.n_q + 2 * tc::BQ - 1) / (2 * tc::BQ), a.heads, B),
+  return launch_pdl(tc::window_attention_tc_kernel, dim3((a.n_q + tc::BQ - 1) / tc::BQ, a.heads, B),
                     dim3(tc::THREADS), tc::SMEM, st, tq, tk, tv, a, spans, err);
 }
 
-// Up to this many query rows a key head, 16-row tiles; above, 128-row tiles.
-constexpr int kFewRows = 64;
+// Rows are few where 16-row tiles are hardly more than 128-row ones (per key head; both
+// read the same keys), whatever the batch, so that a row's result does not depend on it.
+// Over 1028 of 4352 keys, us for 16-row tiles (128-row tiles): 24 key heads, 1 query 7.0
+// (14.0), 16 queries 7.3 (15.5), 32 queries 8.4 (15.9); 4 sequences, 24 heads on 8 key heads,
+// 1 query 8.0 (16.2), 16 queries 15.6 (16.2), 32 queries 30 (16.2).
+bool few_rows(const WindowArgs& a) {
+  const int64_t group = a.heads / a.kv_heads;
+  return (a.n_q * group + 15) / 16 <= group * ((a.n_q + tc::BQ - 1) / tc::BQ) + 1;
+}
 
 }  // namespace
 
@@ -771,7 +785,7 @@ extern "C" lens_status lens_op_attention_window(const uint16_t* q, const uint16_
                      n_q, n_kv, left < 0 || left > kMaxPos ? kMaxPos : left,
                      right < 0 || right > kMaxPos ? kMaxPos : right, sinks, scale * 1.4426950408889634f};
   cudaStream_t st = (cudaStream_t)stream;
-  if (n_q <= kFewRows) return launch_few(a, spans, B, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
+  if (few_rows(a)) return launch_few(a, spans, B, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
   int* err = op_err_ptr();
   if (!err) return LENS_ERR_CUDA;
   return launch_many(a, spans, B, err, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
