@@ -2,14 +2,18 @@
 // scale between them (lens_op_sandwich_norm):
 //   h' = a h + gate * post_gain * y / rms(y)
 //   out = (1 + scale) * pre_gain * h' / rms(h') + shift      (bf16, or e4m3 with scales)
-// Bound by HBM: h and y are read once and h' and out written once (12 bytes a value with
-// a bf16 branch and output), so a row stays in registers through both norms: a thread
-// holds eight consecutive columns, and each mean is a warp sum plus one barrier.
+// Bound by HBM: h and y are read once and h' and out written once (12 bytes a value with a
+// bf16 branch and output), so a row stays in registers through both norms.  A CTA takes
+// consecutive rows, a thread the same eight columns of each: the vectors of its columns
+// stay in registers (as three: gate * post_gain, (1 + scale) * pre_gain, shift) until the
+// sample changes, the next row is loaded before this one's sums, and each mean is a warp
+// sum plus one barrier.
 #include <math.h>
 
 #include "f8.cuh"
 #include "kernels.cuh"
 #include "lens_dit.h"
+#include "smem_attr.h"
 
 namespace lens {
 
@@ -27,15 +31,19 @@ struct SandwichArgs {
   float residual_scale, eps;
 };
 
-// Sum over the CTA; the buffer is free again once every thread has passed the next
-// barrier, so two buffers taken in turn need one barrier a sum.
+// Sum over the CTA of the warps' sums; buf holds zeros past the last warp.  The buffer is
+// free again once every thread has passed the next barrier, so two buffers taken in turn
+// need one barrier a sum.
 __device__ __forceinline__ float cta_sum(float s, float* buf) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = s;
   __syncthreads();
   float t = 0.f;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) t += buf[w];
+  for (int w = 0; w < (int)(blockDim.x >> 5); w += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(buf + w);
+    t += (q.x + q.y) + (q.z + q.w);
+  }
   return t;
 }
 
@@ -48,53 +56,128 @@ __device__ __forceinline__ void load8_or(const float* p, int64_t i, float other,
   }
 }
 
-template <bool Y_BF16, bool OUT_F8>
-__global__ void __launch_bounds__(1024) sandwich_norm_kernel(const SandwichArgs a) {
-  __shared__ float red[2][32];
-  const int row = blockIdx.x, col = 8 * threadIdx.x;
+// 8 values of the branch's output as they are stored
+template <bool BF16>
+struct Branch8 {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    a = f[0], b = f[1];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <>
+struct Branch8<true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = bf16lo(u.x), v[1] = bf16hi(u.x), v[2] = bf16lo(u.y), v[3] = bf16hi(u.y);
+    v[4] = bf16lo(u.z), v[5] = bf16hi(u.z), v[6] = bf16lo(u.w), v[7] = bf16hi(u.w);
+  }
+};
+
+// 1 / rms from the sum of squares.  Correctly rounded: the approximate reciprocal root is
+// up to 2 units off for a whole row, which moves five times as many 8-bit codes as the
+// rounding of the terms does.
+__device__ __forceinline__ float inv_rms(float sum, int D, float eps) { return __frsqrt_rn(sum / D + eps); }
+
+template <int THREADS, bool Y_BF16, bool OUT_F8>
+__global__ void __launch_bounds__(THREADS) sandwich_norm_kernel(const __grid_constant__ SandwichArgs a) {
+  __shared__ __align__(16) float red[2][32];
+  const int col = 8 * threadIdx.x;
   const bool on = col < a.D;
-  const int64_t mod = (int64_t)(row / a.rows_per_batch) * a.mod_stride + col, at = (int64_t)row * a.D + col;
-  float h[8] = {}, y[8] = {}, g[8], p[8];
-  float s = 0.f;
-  if (on) {
-    load8<false>(a.h, at, h);
-    load8<Y_BF16>(a.y, at, y);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s += y[j] * y[j];
-  }
-  float r = __frsqrt_rn(cta_sum(s, red[0]) / a.D + a.eps);
-  s = 0.f;
-  if (on) {
-    load8_or(a.gate, mod, 1.f, g);
-    load8_or(a.post_gain, col, 1.f, p);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[j] = fmaf(g[j] * p[j], y[j] * r, a.residual_scale * h[j]);
-      s += h[j] * h[j];
+  int row = (int)((int64_t)a.M * blockIdx.x / gridDim.x);
+  const int end = (int)((int64_t)a.M * (blockIdx.x + 1) / gridDim.x);
+  if (threadIdx.x < 64) red[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
+  for (int i = blockDim.x + threadIdx.x; i < 64; i += blockDim.x) red[i >> 5][i & 31] = 0.f;
+  __syncthreads();
+  grid_dependency_sync();
+  int sample_end = row;                              // the vectors below are those of rows before it
+  float gp[8], sp[8], sh[8];
+  float4 h0, h1;
+  Branch8<Y_BF16> y;
+  auto load = [&](int r) {
+    if (on && r < end) {
+      const int64_t at = (int64_t)r * a.D + col;
+      const float4* f = reinterpret_cast<const float4*>(a.h + at);
+      h0 = f[0], h1 = f[1];
+      y.load(a.y, at);
     }
-    float4* o = reinterpret_cast<float4*>(a.h_out + at);
-    o[0] = make_float4(h[0], h[1], h[2], h[3]);
-    o[1] = make_float4(h[4], h[5], h[6], h[7]);
-  }
-  r = __frsqrt_rn(cta_sum(s, red[1]) / a.D + a.eps);
-  if (on) {
-    load8_or(a.scale, mod, 0.f, g);
-    load8_or(a.pre_gain, col, 1.f, p);
+  };
+  load(row);
+  for (; row < end; ++row) {
+    if (row >= sample_end) {
+      const int sample = row / a.rows_per_batch;
+      sample_end = min((int64_t)(sample + 1) * a.rows_per_batch, (int64_t)end);
+      if (on) {
+        const int64_t mod = (int64_t)sample * a.mod_stride + col;
+        float p[8];
+        load8_or(a.gate, mod, 1.f, gp);
+        load8_or(a.post_gain, col, 1.f, p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = (1.f + g[j]) * p[j] * (h[j] * r);
-    load8_or(a.shift, mod, 0.f, g);
+        for (int j = 0; j < 8; ++j) gp[j] *= p[j];
+        load8_or(a.scale, mod, 0.f, sp);
+        load8_or(a.pre_gain, col, 1.f, p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] += g[j];
+        for (int j = 0; j < 8; ++j) sp[j] = (1.f + sp[j]) * p[j];
+        load8_or(a.shift, mod, 0.f, sh);
+      }
+    }
+    const int64_t at = (int64_t)row * a.D + col;
+    float h[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w}, v[8];
+    y.get(v);
+    load(row + 1);
+    float s = 0.f;
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j] * v[j];
+    }
+    float r = inv_rms(cta_sum(s, red[0]), a.D, a.eps);
+    s = 0.f;
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        h[j] = fmaf(gp[j], v[j] * r, a.residual_scale * h[j]);
+        s += h[j] * h[j];
+      }
+      float4* o = reinterpret_cast<float4*>(a.h_out + at);
+      o[0] = make_float4(h[0], h[1], h[2], h[3]);
+      o[1] = make_float4(h[4], h[5], h[6], h[7]);
+    }
+    r = inv_rms(cta_sum(s, red[1]), a.D, a.eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = on ? fmaf(sp[j], h[j] * r, sh[j]) : 0.f;
+    if constexpr (OUT_F8) {
+      float scale, inv;
+      f8_scale(half_warp_max(amax8(h)), scale, inv);     // idle lanes hold zeros
+      if (on) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) = f8_pack8(h, inv);
+        if ((threadIdx.x & 15) == 0) a.out_scales[(int64_t)(col / kF8Group) * a.M + row] = scale;
+      }
+    } else if (on) {
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at) = make_uint4(
+          pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]), pack_bf16x2(h[4], h[5]), pack_bf16x2(h[6], h[7]));
+    }
   }
-  if constexpr (OUT_F8) {
-    float scale, inv;
-    f8_scale(half_warp_max(amax8(h)), scale, inv);     // idle lanes hold zeros
-    if (on) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) = f8_pack8(h, inv);
-    if (on && (threadIdx.x & 15) == 0) a.out_scales[(int64_t)(col / kF8Group) * a.M + row] = scale;
-  } else if (on) {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at) =
-        make_uint4(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]), pack_bf16x2(h[4], h[5]), pack_bf16x2(h[6], h[7]));
-  }
+}
+
+template <bool Y_BF16, bool OUT_F8>
+cudaError_t launch_sandwich(const SandwichArgs& a, int sms, cudaStream_t st) {
+  const int threads = (a.D / 8 + 31) / 32 * 32;
+#ifndef VT
+#define VT 768
+#endif
+  const int per_sm = VT / threads > 0 ? (VT / threads > 16 ? 16 : VT / threads) : 1;
+  const int grid = a.M < sms * per_sm ? a.M : sms * per_sm;
+  if (threads <= 256)
+    return launch_pdl(sandwich_norm_kernel<256, Y_BF16, OUT_F8>, dim3(grid), dim3(threads), 0, st, a);
+  if (threads <= 512)
+    return launch_pdl(sandwich_norm_kernel<512, Y_BF16, OUT_F8>, dim3(grid), dim3(threads), 0, st, a);
+  return launch_pdl(sandwich_norm_kernel<1024, Y_BF16, OUT_F8>, dim3(grid), dim3(threads), 0, st, a);
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -123,16 +206,10 @@ extern "C" lens_status lens_op_sandwich_norm(const float* h, const void* y, lens
     return LENS_ERR_INVALID_ARG;
   const SandwichArgs a{h,   y,          post_gain,  gate, pre_gain, shift,          scale,         h_out,
                        out, out_scales, mod_stride, M,    D,        rows_per_batch, residual_scale, eps};
-  const int threads = (D / 8 + 31) / 32 * 32;
   cudaStream_t st = (cudaStream_t)stream;
   const bool yb = y_type == LENS_BF16, of8 = out_type == LENS_F8E4M3;
-  if (yb && of8)
-    sandwich_norm_kernel<true, true><<<M, threads, 0, st>>>(a);
-  else if (yb)
-    sandwich_norm_kernel<true, false><<<M, threads, 0, st>>>(a);
-  else if (of8)
-    sandwich_norm_kernel<false, true><<<M, threads, 0, st>>>(a);
-  else
-    sandwich_norm_kernel<false, false><<<M, threads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
+  const int sms = device_sms();
+  const cudaError_t e = yb ? (of8 ? launch_sandwich<true, true>(a, sms, st) : launch_sandwich<true, false>(a, sms, st))
+                           : (of8 ? launch_sandwich<false, true>(a, sms, st) : launch_sandwich<false, false>(a, sms, st));
+  return e == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
 }
