@@ -4,77 +4,83 @@
 #include "f8_gemm.h"
 #include "kernels.cuh"
 #include "lens_dit.h"
+#include "smem_attr.h"
 
 namespace lens {
 
 namespace {
 
 // ------------------------------------------------------------------ quantization
-// Bound by HBM: each value is read once and its code written once.  A half warp owns a
-// block row of 128 (eight values a lane, so the largest is four shuffles away).
+// Bound by HBM: each value is read once and its code written once.
 //
-// A scale per row and 128 columns: a CTA takes 32 rows of one 128-wide column block, and
-// stores their scales as one contiguous piece.
+// A scale per row and 128 columns: eight lanes own a block (16 values each, so that the
+// shuffles and the division are shared by many), a CTA takes eight rows of four 128-wide
+// column blocks (1 KB of a bf16 row in one piece).  4352 x 4096 bf16: 11.7 us, 4.6 TB/s with
+// the launch (13.6 with 16 lanes a block, both divisions in each and 32 rows of one block).
 template <bool BF16>
 __global__ void __launch_bounds__(256) quantize_f8_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t k,
                                                                uint8_t* __restrict__ codes,
                                                                float* __restrict__ scales) {
-  __shared__ float s_scale[32];
-  const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int64_t g = blockIdx.y, r0 = (int64_t)blockIdx.x * 32;
-  const int64_t col = g * kF8Group + 8 * l;
-  float v[2][8];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t r = r0 + half + 16 * i;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    if (r < rows && col < k) load8<BF16>(x, r * k + col, v[i]);
+  __shared__ float s_scale[4][8];
+  const int l = threadIdx.x & 7, block = (threadIdx.x >> 3) & 3, row = threadIdx.x >> 5;
+  const int64_t g = (int64_t)blockIdx.y * 4 + block, r = (int64_t)blockIdx.x * 8 + row;
+  const int64_t col = g * kF8Group + 16 * l;
+  const bool on = r < rows && col < k;
+  grid_dependency_sync();
+  float v[2][8] = {};
+  if (on) {
+    load8<BF16>(x, r * k + col, v[0]);
+    load8<BF16>(x, r * k + col + 8, v[1]);
   }
+  float m = max_nan(amax8(v[0]), amax8(v[1])), scale, inv;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t r = r0 + half + 16 * i;
-    float scale, inv;
-    f8_scale(half_warp_max(amax8(v[i])), scale, inv);
-    if (r < rows && col < k) *reinterpret_cast<uint2*>(codes + r * k + col) = f8_pack8(v[i], inv);
-    if (l == 0) s_scale[half + 16 * i] = scale;
+  for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  f8_scale(m, scale, inv);
+  if (on) {
+    const uint2 a = f8_pack8(v[0], inv), b = f8_pack8(v[1], inv);
+    *reinterpret_cast<uint4*>(codes + r * k + col) = make_uint4(a.x, a.y, b.x, b.y);
   }
+  if (l == 0) s_scale[block][row] = scale;
   __syncthreads();
-  if (threadIdx.x < 32 && r0 + threadIdx.x < rows) scales[g * rows + r0 + threadIdx.x] = s_scale[threadIdx.x];
+  if (threadIdx.x < 32) {
+    const int64_t rr = (int64_t)blockIdx.x * 8 + (threadIdx.x & 7), gg = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 3);
+    if (rr < rows && gg * kF8Group < k) scales[gg * rows + rr] = s_scale[threadIdx.x >> 3][threadIdx.x & 7];
+  }
 }
 
-// A scale per 128 x 128 block: one CTA per block, its values held in registers between
-// the maximum and the rounding.
+// A scale per 128 x 128 block: one CTA per block, half a warp a row of it, its values held in
+// registers between the maximum and the rounding.
 template <bool BF16>
-__global__ void __launch_bounds__(256) quantize_f8_blocks_kernel(const void* __restrict__ x, int64_t rows, int64_t k,
+__global__ void __launch_bounds__(512) quantize_f8_blocks_kernel(const void* __restrict__ x, int64_t rows, int64_t k,
                                                                  uint8_t* __restrict__ codes,
                                                                  float* __restrict__ scales) {
-  __shared__ float s_max[8];
+  __shared__ float s_max[16];
   const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
   const int64_t g = blockIdx.y, r0 = (int64_t)blockIdx.x * kF8Group;
   const int64_t col = g * kF8Group + 8 * l;
-  float v[8][8];
+  grid_dependency_sync();
+  float v[4][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + half + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + half + 32 * i;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
     if (r < rows && col < k) load8<BF16>(x, r * k + col, v[i]);
   }
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_nan(m, amax8(v[i]));
+  for (int i = 0; i < 4; ++i) m = max_nan(m, amax8(v[i]));
   m = half_warp_max(m);
   m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_nan(m, s_max[i]);
+  for (int i = 0; i < 16; ++i) m = max_nan(m, s_max[i]);
   float scale, inv;
   f8_scale(m, scale, inv);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + half + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + half + 32 * i;
     if (r < rows && col < k) *reinterpret_cast<uint2*>(codes + r * k + col) = f8_pack8(v[i], inv);
   }
   if (threadIdx.x == 0) scales[g * gridDim.x + blockIdx.x] = scale;
@@ -83,20 +89,14 @@ __global__ void __launch_bounds__(256) quantize_f8_blocks_kernel(const void* __r
 cudaError_t launch_quantize_f8(const void* x, bool bf16, int64_t rows, int64_t k, int block_rows, uint8_t* codes,
                                float* scales, cudaStream_t st) {
   const unsigned groups = (unsigned)((k + kF8Group - 1) / kF8Group);
-  const int per = block_rows == 1 ? 32 : kF8Group;
-  const dim3 grid((unsigned)((rows + per - 1) / per), groups);
   if (block_rows == 1) {
-    if (bf16)
-      quantize_f8_rows_kernel<true><<<grid, 256, 0, st>>>(x, rows, k, codes, scales);
-    else
-      quantize_f8_rows_kernel<false><<<grid, 256, 0, st>>>(x, rows, k, codes, scales);
-  } else {
-    if (bf16)
-      quantize_f8_blocks_kernel<true><<<grid, 256, 0, st>>>(x, rows, k, codes, scales);
-    else
-      quantize_f8_blocks_kernel<false><<<grid, 256, 0, st>>>(x, rows, k, codes, scales);
+    const dim3 grid((unsigned)((rows + 7) / 8), (groups + 3) / 4);
+    return launch_pdl(bf16 ? quantize_f8_rows_kernel<true> : quantize_f8_rows_kernel<false>, grid, dim3(256), 0, st, x,
+                      rows, k, codes, scales);
   }
-  return cudaGetLastError();
+  const dim3 grid((unsigned)((rows + kF8Group - 1) / kF8Group), groups);
+  return launch_pdl(bf16 ? quantize_f8_blocks_kernel<true> : quantize_f8_blocks_kernel<false>, grid, dim3(512), 0, st, x,
+                    rows, k, codes, scales);
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

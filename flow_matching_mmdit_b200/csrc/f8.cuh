@@ -26,11 +26,16 @@ __device__ __forceinline__ uint32_t f8_pack2(float lo, float hi) {
   return r;
 }
 
-// scale and its inverse of a block with largest magnitude amax
+// Scale and its inverse of a block with largest magnitude amax, the same in neighbouring
+// lanes (all 32 lanes must call): an even lane divides for the scale, an odd one for the
+// inverse, since two correctly rounded divisions cost as much as eight values otherwise do.
 __device__ __forceinline__ void f8_scale(float amax, float& scale, float& inv) {
   const float a = max_nan(amax, kF8AmaxFloor);
-  scale = __fdiv_rn(a, kF8Max);
-  inv = __fdiv_rn(kF8Max, a);
+  const bool odd = threadIdx.x & 1;
+  const float mine = __fdiv_rn(odd ? kF8Max : a, odd ? a : kF8Max);
+  const float other = __shfl_xor_sync(0xffffffffu, mine, 1);
+  scale = odd ? other : mine;
+  inv = odd ? mine : other;
 }
 
 __device__ __forceinline__ float amax8(const float (&v)[8]) {
