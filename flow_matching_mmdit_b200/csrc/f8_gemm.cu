@@ -15,14 +15,14 @@ namespace lens {
 namespace {
 
 // ------------------------------------------------------------------ tcgen05, CTA pairs
-// 256 x 128 tiles by a cluster of two CTAs (cta_group::2, kind::f8f6f4), persistent.  The
-// scales differ from one 128-wide k block to the next, so a tile's sum over
+// 256 x (128 HALVES) tiles by a cluster of two CTAs (cta_group::2, kind::f8f6f4),
+// persistent.  The scales differ from one 128-wide k block to the next, so a tile's sum over
 // k cannot stay in the tensor cores' accumulator: each block's P_g goes to its own TMEM slot
-// (four of them in turn), and eight epilogue warps read it, scale it and add it to the
-// tile's sum in registers (64 a thread) while the tensor cores work on the next.
-//   warp 0       TMA: 128 rows of A and 64 rows of W of each k block (128-byte rows)
+// (4 / HALVES of them in turn), and eight epilogue warps read it, scale it and add it to the
+// tile's sum in registers (64 HALVES a thread) while the tensor cores work on the next.
+//   warp 0       TMA: 128 rows of A and 64 HALVES rows of W of each k block (128-byte rows)
 //   warps 1, 2   MMA issuers (leader CTA) of the even and the odd k blocks: 4 x (M = 256,
-//                N = 128, K = 32) into a slot.  Blocks do not depend on each other,
+//                N = 128 HALVES, K = 32) into a slot.  Blocks do not depend on each other,
 //                and one thread's two waits, four MMAs and two commits a block take longer
 //                than the MMAs themselves.
 //   warp 3       copies a block's scales beside its slot (cp.async), so that no load's
@@ -34,18 +34,24 @@ namespace {
 //   tfull[j]   (both)    slot j holds a k block's P_g, and its scales have landed
 //   tempty[j]  (leader)  both CTAs' epilogue warps have read slot j
 //   sfree[j]   (each)    this CTA's epilogue warps have read slot j's scales
-// Measured at 8704 x 8192 x 1536: 118 us.  Per k block and pair that is 330 ns: the MMAs
-// alone would take 150, and L2 delivers a pair's 48 KB in 230 (10 TB/s, as for the bf16
+// Per k block and pair of a 256 x 128 tile about 330 ns pass at 8704 x 8192 x 1536: the MMAs
+// alone would take 150 and L2 delivers a pair's 48 KB in 230 (10 TB/s, as for the bf16
 // products); the rest is the way through a slot (MMA, commit, read, release, next MMA), of
-// which four run at a time.  256 x 256 tiles halve W's traffic but leave two slots and gain
-// 5 % at that size and lose 10 to 40 % below it, so there is one tile shape.
-constexpr int BN = 128, COLS = BN / 2;                // COLS: columns a thread accumulates
-constexpr uint32_t A_BYTES = 128 * 128, B_BYTES = (BN / 2) * 128, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int STAGES = 7, SLOTS = 512 / BN;
-constexpr int SCALES = 132;                           // of a slot: 128 rows, the column block
-constexpr uint32_t EPI_BYTES = 8 * 4096, SCALE_BYTES = SLOTS * SCALES * 4, BAR_BYTES = 512;
-constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_BYTES + SCALE_BYTES + BAR_BYTES;
-static_assert(SMEM <= 232448, "shared memory");
+// which four run at a time, or two of twice the width.
+// SPLIT: a cluster of several pairs works on one tile, each on its part of the k blocks, and
+// joins the parts through distributed shared memory.
+template <int HALVES>
+struct F8Cfg {
+  static constexpr int BN = 128 * HALVES, COLS = BN / 2;   // COLS: columns a thread accumulates
+  static constexpr uint32_t A_BYTES = 128 * 128, HALF_BYTES = 64 * 128, B_BYTES = HALVES * HALF_BYTES;
+  static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = HALVES == 1 ? 7 : 6;
+  static constexpr int SLOTS = 4 / HALVES;                // TMEM slots, a k block each
+  static constexpr int SCALES = 132;                       // of a slot: 128 rows, the column blocks
+  static constexpr uint32_t EPI_BYTES = 8 * 4096, SCALE_BYTES = SLOTS * SCALES * 4, BAR_BYTES = 512;
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_BYTES + SCALE_BYTES + BAR_BYTES;
+  static_assert(SMEM <= 232448, "shared memory");
+};
 constexpr int THREADS = 384;
 
 // 4 bytes global -> shared without registers; zero when !live
@@ -59,23 +65,36 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ float4 ld_cluster4(const float4* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(mapa_shared(smem_u32(p), rank))
+               : "memory");
+  return v;
+}
+
 struct F8GemmArgs {
+  void* C;
   int M, N, kblocks, tiles_m, total_tiles, nblocks;
   const float *as, *ws, *bias;
   int* err;
 };
 
-template <bool BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+template <int HALVES, bool BF16, int SPLITS>
+__global__ void __launch_bounds__(THREADS, 1)
     gemm_f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmC, const F8GemmArgs a) {
+  using C = F8Cfg<HALVES>;
+  constexpr bool SPLIT = SPLITS > 1;
+  constexpr int STAGES = C::STAGES, SLOTS = C::SLOTS, BN = C::BN, COLS = C::COLS, SCALES = C::SCALES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
-  uint8_t* sW = smem + STAGES * A_BYTES;
-  uint8_t* sEpi = sW + STAGES * B_BYTES;
-  float* sScale = reinterpret_cast<float*>(sEpi + EPI_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + EPI_BYTES + SCALE_BYTES);
+  uint8_t* sW = smem + STAGES * C::A_BYTES;
+  uint8_t* sEpi = sW + STAGES * C::B_BYTES;
+  float* sScale = reinterpret_cast<float*>(sEpi + C::EPI_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES + C::SCALE_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + SLOTS;
@@ -83,11 +102,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint64_t* drain = sfree + SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   uint32_t* peer_issued = tmem_slot + 1;
-  static_assert((2 * STAGES + 3 * SLOTS + 2) * 8 + 8 <= BAR_BYTES, "barriers overflow their reserve");
+  static_assert((2 * STAGES + 3 * SLOTS + 2) * 8 + 8 <= C::BAR_BYTES, "barriers overflow their reserve");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  // this CTA's rank in its pair, and the pair's leader in the cluster
+  const uint32_t rank = SPLIT ? cluster_ctarank() & 1 : cluster_ctarank(), base = SPLIT ? cluster_ctarank() & ~1u : 0;
+  const uint16_t both = 0x3 << base;
+  // SPLIT: one tile a cluster, the k blocks [kb0, kb1) of it a pair
+  const int pair = SPLIT ? blockIdx.x / (2 * SPLITS) : blockIdx.x >> 1, npairs = SPLIT ? a.total_tiles : gridDim.x >> 1;
+  const int kb0 = SPLIT ? a.kblocks * (int)(base >> 1) / SPLITS : 0;
+  const int kb1 = SPLIT ? a.kblocks * (int)((base >> 1) + 1) / SPLITS : a.kblocks;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -119,19 +143,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   uint32_t prod_issued = 0;
   bool prod_ok = true;
+  // 128 sums and 64 loaded columns a thread do not fit an even share of the registers: the
+  // epilogue's two warpgroups take over what the first gives up (72 + 2 x 216 = 3 x 168)
+  if (warp < 4) {
+  if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
       for (int t = pair; t < a.total_tiles && prod_ok; t += npairs) {
         const int tn = t / a.tiles_m, m0 = (t - tn * a.tiles_m) * 256 + 128 * (int)rank, n0 = tn * BN + (BN / 2) * (int)rank;
-        for (int kb = 0; kb < a.kblocks; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, a.err)) {
             prod_ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx(&full[stage], 2 * STAGE_BYTES);
-          tma_load_2d_pair(sA + stage * A_BYTES, &tmA, &full[stage], kb * 128, m0);
-          tma_load_2d_pair(sW + stage * B_BYTES, &tmW, &full[stage], kb * 128, n0);
+          if (rank == 0) mbar_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+          tma_load_2d_pair(sA + stage * C::A_BYTES, &tmA, &full[stage], kb * 128, m0);
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_2d_pair(sW + stage * C::B_BYTES + h * C::HALF_BYTES, &tmW, &full[stage], kb * 128, n0 + 64 * h);
           ++prod_issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -140,7 +170,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
       // the leader reconciles both CTAs' loads if the pair aborts
-      if (rank == 1) st_shared_cluster_u32(mapa_shared(smem_u32(peer_issued), 0), prod_issued);
+      if (rank == 1) st_shared_cluster_u32(mapa_shared(smem_u32(peer_issued), base), prod_issued);
     }
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
@@ -149,19 +179,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const uint32_t odd = warp == 2;
       bool ok = true;
       uint32_t stage = odd, phase = 0, slot = odd, use = 0;
-      const int64_t blocks = (int64_t)((a.total_tiles - pair + npairs - 1) / npairs) * a.kblocks;
+      const int64_t blocks = (int64_t)((a.total_tiles - pair + npairs - 1) / npairs) * (kb1 - kb0);
       for (int64_t i = odd; i < blocks; i += 2) {
         if (!mbar_wait_sleep(&tempty[slot], use ^ 1, a.err) || !mbar_wait_sleep(&full[stage], phase, a.err)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint64_t ad = umma_desc_sw128(smem_u32(sA + stage * A_BYTES));
-        const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * B_BYTES));
+        const uint64_t ad = umma_desc_sw128(smem_u32(sA + stage * C::A_BYTES));
+        const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * C::B_BYTES));
 #pragma unroll
         for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + slot * BN, ad + 2 * k, wd + 2 * k, idesc, k > 0 ? 1u : 0u);
-        umma_commit_pair(&empty[stage], 0x3);
-        umma_commit_pair(&tfull[slot], 0x3);
+        umma_commit_pair(&empty[stage], both);
+        umma_commit_pair(&tfull[slot], both);
         if ((stage += 2) >= STAGES) {
           stage -= STAGES;
           phase ^= 1;
@@ -171,17 +201,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           use ^= 1;
         }
       }
-      if (!ok) umma_drain_pair(&drain[odd]);
+      if (!ok) umma_drain_pair(&drain[odd], (uint16_t)(1u << base));
     }
     __syncwarp();
-  } else if (warp == 3) {
+  } else {
     uint32_t slot = 0, use = 0;
     bool ok = true;
     for (int t = pair; t < a.total_tiles && ok; t += npairs) {
       const int tn = t / a.tiles_m, row = (t - tn * a.tiles_m) * 256 + 128 * (int)rank + lane;
-      const float* pa = a.as + row;
-      const float* pw = a.ws + tn;             // a tile's columns are one block of W's scales
-      for (int kb = 0; kb < a.kblocks; ++kb) {
+      const float* pa = a.as + (int64_t)kb0 * a.M + row;
+      // a column block past the last one holds no output: any block's scale will do
+      const float* pw = a.ws + (int64_t)kb0 * a.nblocks + min(tn * HALVES + (lane & (HALVES - 1)), a.nblocks - 1);
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sfree[slot], use ^ 1, a.err))) {
           ok = false;
           break;
@@ -192,7 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const bool live = row + 32 * i < a.M;
           cp_async4(dst + lane + 32 * i, live ? pa + 32 * i : a.as, live);
         }
-        if (lane == 0) cp_async4(dst + 128, pw, true);
+        if (lane < HALVES) cp_async4(dst + 128 + lane, pw, true);
         cp_async_arrive(&tfull[slot]);
         pa += a.M;
         pw += a.nblocks;
@@ -204,13 +235,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     cp_async_wait_all();
     __syncwarp();
+  }
   } else {
+    if constexpr (HALVES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3, part = (warp - 4) >> 2;
     uint8_t* box = sEpi + (warp - 4) * 4096;
     const uint32_t lane_addr = tmem + (uint32_t(quarter * 32) << 16) + part * COLS;
-    const uint32_t leader_tempty = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t leader_tempty = mapa_shared(smem_u32(&tempty[0]), base);
     const float* a_scale = sScale + quarter * 32 + lane;
-    const float* w_scale = sScale + 128;
+    const float* w_scale = sScale + 128 + (HALVES == 1 ? 0 : part);
     uint32_t slot = 0, use = 0, no_box = 0;
     bool ok = true, ready = false;
     for (int t = pair; t < a.total_tiles && ok; t += npairs) {
@@ -218,39 +251,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
 #pragma unroll 1
-      for (int kb = 0; kb < a.kblocks; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!__all_sync(0xffffffffu, ready) && !__all_sync(0xffffffffu, mbar_wait(&tfull[slot], use, a.err))) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t at = lane_addr + slot * BN;
-        float r[2][32];
-        tmem_ld32(at, r[0]);
-        tmem_ld32(at + 32, r[1]);
+        constexpr int PIECE = 64;
+        float r[PIECE / 32][32];
+#pragma unroll
+        for (int i = 0; i < PIECE / 32; ++i) tmem_ld32(at + 32 * i, r[i]);
         const float s = a_scale[slot * SCALES] * w_scale[slot * SCALES];
         const uint64_t s2 = f2_pack(s, s);
-        tmem_ld_wait(r[0]);
-        tmem_ld_pin(r[1]);
-        // everything is in registers: the slot may be filled again
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_remote(leader_tempty + slot * 8);
-          mbar_arrive(&sfree[slot]);
-        }
-        if (++slot == SLOTS) {
-          slot = 0;
-          use ^= 1;
-        }
-        ready = mbar_test(&tfull[slot], use);    // asked ahead of the adds that hide it
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          acc[i] = f2_fma(f2_pack(r[i / 16][2 * (i % 16)], r[i / 16][2 * (i % 16) + 1]), s2, acc[i]);
+        for (int c = 0; c < COLS / PIECE; ++c) {
+          tmem_ld_wait(r[0]);
+          tmem_ld_pin(r[1]);
+          if (c + 1 == COLS / PIECE) {
+            // everything is in registers: the slot may be filled again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_remote(leader_tempty + slot * 8);
+              mbar_arrive(&sfree[slot]);
+            }
+            if (++slot == SLOTS) {
+              slot = 0;
+              use ^= 1;
+            }
+            ready = mbar_test(&tfull[slot], use);    // asked ahead of the adds that hide it
+          }
+#pragma unroll
+          for (int i = 0; i < PIECE / 2; ++i)
+            acc[PIECE / 2 * c + i] = f2_fma(f2_pack(r[i / 16][2 * (i % 16)], r[i / 16][2 * (i % 16) + 1]), s2,
+                                            acc[PIECE / 2 * c + i]);
+          if (c + 1 < COLS / PIECE)
+#pragma unroll
+            for (int i = 0; i < PIECE / 32; ++i) tmem_ld32(at + PIECE * (c + 1) + 32 * i, r[i]);
+        }
       }
       if (!ok) break;
       const int tn = t / a.tiles_m, row0 = (t - tn * a.tiles_m) * 256 + 128 * (int)rank + quarter * 32;
       const int n0 = tn * BN + part * COLS;
+      if constexpr (SPLIT) {
+        // this pair's part of the sum, [part][16-byte piece of the columns][row]; the stages
+        // are free: every MMA has completed
+        float4* mine = reinterpret_cast<float4*>(smem) + part * 16 * 128 + quarter * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float4 v;
+          f2_unpack(acc[2 * c], v.x, v.y);
+          f2_unpack(acc[2 * c + 1], v.z, v.w);
+          mine[128 * c] = v;
+        }
+        continue;
+      }
       constexpr int PER = BF16 ? 64 : 32;        // columns of one 128-byte box row
 #pragma unroll
       for (int c = 0; c < COLS / PER; ++c) {
@@ -281,38 +337,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 
   tc_fence_before();
-  cluster_sync_all();          // every role of both CTAs has left its loop
+  cluster_sync_all();          // every role of the cluster's CTAs has left its loop
+  if constexpr (SPLIT) {
+    // each of the cluster's pairs finishes a share of the columns, adding the pairs' parts in order
+    if (warp >= 4 && !err_raised(a.err)) {
+      const int quarter = warp & 3, part = (warp - 4) >> 2, tn = pair / a.tiles_m;
+      const int row = (pair - tn * a.tiles_m) * 256 + 128 * (int)rank + quarter * 32 + lane;
+      constexpr int SHARE = 16 / SPLITS;
+      const int first = SHARE * (int)(base >> 1);
+      const float4* mine = reinterpret_cast<const float4*>(smem) + part * 16 * 128 + quarter * 32 + lane;
+      float4 v[SHARE][SPLITS];
+#pragma unroll
+      for (int c = 0; c < SHARE; ++c)
+#pragma unroll
+        for (int p = 0; p < SPLITS; ++p) v[c][p] = ld_cluster4(mine + 128 * (first + c), 2 * p + rank);
+#pragma unroll
+      for (int c = 0; c < SHARE; ++c) {
+        const int n = tn * BN + part * COLS + 4 * (first + c);
+        if (row >= a.M || n >= a.N) continue;
+        float4 y = v[c][0];
+#pragma unroll
+        for (int p = 1; p < SPLITS; ++p) y.x += v[c][p].x, y.y += v[c][p].y, y.z += v[c][p].z, y.w += v[c][p].w;
+        if (a.bias) {
+          y.x += __ldg(a.bias + n), y.y += __ldg(a.bias + n + 1);
+          y.z += __ldg(a.bias + n + 2), y.w += __ldg(a.bias + n + 3);
+        }
+        const int64_t at = (int64_t)row * a.N + n;
+        if (BF16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.C) + at) =
+              make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(a.C) + at) = y;
+      }
+    }
+  }
   if (warp == 0 && lane == 0 && rank == 0 && (!prod_ok || err_raised(a.err)))
-    drain_pair_stages<STAGES>(full, [&](uint32_t) { return STAGE_BYTES; }, prod_issued, *peer_issued);
-  cluster_sync_all();          // no MMA, TMA or remote arrive of the pair is in flight
+    drain_pair_stages<STAGES>(full, [&](uint32_t) { return C::STAGE_BYTES; }, prod_issued, *peer_issued);
+  cluster_sync_all();          // no MMA, TMA, remote arrive or remote read of the cluster is in flight
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
 }
 
-template <bool BF16>
+template <int HALVES, bool BF16, int SPLITS>
 cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
+  using C = F8Cfg<HALVES>;
   CUtensorMap ta, tw, tc;
   if (!encode_tmap_u8(&ta, g.A, g.M, g.K, 128) || !encode_tmap_u8(&tw, g.W, g.N, g.K, 64) ||
       !encode_tmap_out(&tc, g.C, BF16 ? 2 : 4, g.M, g.N, g.N))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> attr{0};
-  const cudaError_t e = ensure_smem_limit(gemm_f8_pair_kernel<BF16>, (int)SMEM, attr);
+  const auto kernel = gemm_f8_pair_kernel<HALVES, BF16, SPLITS>;
+  const cudaError_t e = ensure_smem_limit(kernel, (int)C::SMEM, attr);
   if (e != cudaSuccess) return e;
   F8GemmArgs a;
+  a.C = g.C;
   a.M = g.M;
   a.N = g.N;
   a.kblocks = (g.K + kF8Group - 1) / kF8Group;
   a.nblocks = (g.N + kF8Group - 1) / kF8Group;
   a.tiles_m = (g.M + 255) / 256;
-  a.total_tiles = a.tiles_m * ((g.N + BN - 1) / BN);
+  a.total_tiles = a.tiles_m * ((g.N + C::BN - 1) / C::BN);
   a.as = g.a_scales;
   a.ws = g.w_scales;
   a.bias = g.bias;
   a.err = err;
-  const int pairs = a.total_tiles < sms / 2 ? a.total_tiles : sms / 2;
-  return launch_pdl(gemm_f8_pair_kernel<BF16>, dim3(2 * pairs), dim3(THREADS), SMEM, st, ta, tw, tc, a);
+  const int pairs = SPLITS > 1 ? a.total_tiles * SPLITS : (a.total_tiles < sms / 2 ? a.total_tiles : sms / 2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2 * SPLITS;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, ta, tw, tc, a);
+}
+
+template <int HALVES, int SPLITS>
+cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
+  return g.bf16 ? launch_pair<HALVES, true, SPLITS>(g, err, sms, st)
+                : launch_pair<HALVES, false, SPLITS>(g, err, sms, st);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -410,7 +522,19 @@ cudaError_t launch_gemm_f8(const F8Gemm& g, int* err, int sms, cudaStream_t st) 
   if (g.M <= 8) return launch_few<1>(g, st);
   if (g.M <= 16) return launch_few<2>(g, st);
   if (g.M <= 32) return launch_few<4>(g, st);
-  return g.bf16 ? launch_pair<true>(g, err, sms, st) : launch_pair<false>(g, err, sms, st);
+  const int64_t tiles_m = (g.M + 255) / 256, pairs = sms / 2, kblocks = (g.K + kF8Group - 1) / kF8Group;
+  const int64_t narrow_tiles = tiles_m * ((g.N + 127) / 128), wide_tiles = tiles_m * ((g.N + 255) / 256);
+  // Few tiles and a long k: four pairs a tile, while their clusters of eight CTAs find room
+  // beside each other.  77 x 1536 x 4096 (32 k blocks): 8.4 us for 13.0; 256 x 1536 x 1536 (12):
+  // 7.9 for 7.5, the join costs as much as nine blocks.
+  if (20 * narrow_tiles <= 4 * pairs && kblocks >= 20) return launch_pair<1, 4>(g, err, sms, st);
+  // 256-wide tiles load and wait less a column, but only where their rounds on the pairs
+  // come near half of the 128-wide ones': sustained, us, 8704 x 8192 x 1536 (15 rounds for 30)
+  // 135 for 142, 8704 x 1536 x 4096 (3 for 6) 65 for 72, 4352 x 4608 x 1536 (5 for 9) 43 for
+  // 44, 4352 x 1536 x 4096 (2 for 3) 39 for 37, 1152 x 8192 x 1536 (3 for 5) 26 for 23
+  const int64_t wide = (wide_tiles + pairs - 1) / pairs, narrow = (narrow_tiles + pairs - 1) / pairs;
+  if (7 * wide <= 4 * narrow) return launch_pair<2, 1>(g, err, sms, st);
+  return launch_pair<1, 1>(g, err, sms, st);
 }
 
 }  // namespace lens

@@ -189,10 +189,17 @@ struct KScope {
     LENS_CUDA(x);                   \
   } while (0)
 
+// What a device answers to is looked up once per device ordinal (0: not yet).
+constexpr int kCachedDevices = 64;
+
 int lens::device_sms() {
+  static std::atomic<int> known[kCachedDevices];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  const bool cached = dev >= 0 && dev < kCachedDevices;
+  if (cached && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (cached) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -218,8 +225,14 @@ static GemmProblem base_problem(int M, int N, int K) {
 // Used by the handle-free op entry points.
 __device__ int g_op_err;
 int* lens::op_err_ptr() {
-  int* p = nullptr;
+  static std::atomic<int*> known[kCachedDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  const bool cached = dev >= 0 && dev < kCachedDevices;
+  int* p = cached ? known[dev].load(std::memory_order_relaxed) : nullptr;
+  if (p) return p;
   if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_op_err) != cudaSuccess) return nullptr;
+  if (cached) known[dev].store(p, std::memory_order_relaxed);
   return p;
 }
 

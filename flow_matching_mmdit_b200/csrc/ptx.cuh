@@ -338,8 +338,8 @@ __device__ __forceinline__ void umma_drain(uint64_t* bar) {
 }
 // The same for the leader of a CTA pair (the pair's UMMAs write both CTAs' TMEM);
 // the commit arrives on the leader's `bar` only.
-__device__ __forceinline__ void umma_drain_pair(uint64_t* bar) {
-  umma_commit_pair(bar, 0x1);
+__device__ __forceinline__ void umma_drain_pair(uint64_t* bar, uint16_t leader = 0x1) {
+  umma_commit_pair(bar, leader);
   mbar_wait_drain(bar, 0);
 }
 
