@@ -383,23 +383,51 @@ def lens_op_gemm_w4(A, codes, scales, bias, C, M: int, N: int, K: int, stream=No
                                           _stream(stream)), "lens_op_gemm_w4")
 
 
+def _whole(where: str, stream, *tensors):
+    """Device pointers of whole tensors (None passes NULL), then the stream's, for the operations
+    below: a tensor on another device than the current one, or not contiguous, is refused."""
+    import torch
+    dev, out = None, []
+    for x in tensors:
+        if x is None:
+            out.append(None)
+            continue
+        at = x.get_device()
+        if at != dev:
+            if at < 0 or dev is not None or at != torch.cuda.current_device():
+                raise LensError(1, where)
+            dev = at
+        if not x.is_contiguous():
+            raise LensError(1, where)
+        out.append(x.data_ptr())
+    if stream is None and dev is not None:
+        out.append(torch._C._cuda_getCurrentRawStream(dev) or None)
+    else:
+        out.append(_stream(stream))
+    return out
+
+
 def lens_op_quantize_f8(x, x_type: int, rows: int, k: int, block_rows: int, codes, scales, stream=None) -> None:
-    _check(load_library().lens_op_quantize_f8(_ptr(x), x_type, rows, k, block_rows, _ptr(codes), _ptr(scales),
-                                              _stream(stream)), "lens_op_quantize_f8")
+    px, pc, ps, st = _whole("lens_op_quantize_f8", stream, x, codes, scales)
+    _check(load_library().lens_op_quantize_f8(px, x_type, rows, k, block_rows, pc, ps, st),
+           "lens_op_quantize_f8")
 
 
 def lens_op_gemm_f8(A, a_scales, W, w_scales, bias, C, c_type: int, M: int, N: int, K: int, stream=None) -> None:
-    _check(load_library().lens_op_gemm_f8(_ptr(A), _ptr(a_scales), _ptr(W), _ptr(w_scales), _ptr(bias), _ptr(C), c_type,
-                                          M, N, K, _stream(stream)), "lens_op_gemm_f8")
+    pa, psa, pw, psw, pb, pc, st = _whole("lens_op_gemm_f8", stream, A, a_scales, W, w_scales, bias, C)
+    _check(load_library().lens_op_gemm_f8(pa, psa, pw, psw, pb, pc, c_type, M, N, K, st),
+           "lens_op_gemm_f8")
 
 
 def lens_op_sandwich_norm(h, y, y_type: int, M: int, D: int, rows_per_batch: int, post_gain, gate, pre_gain, shift,
                           scale, mod_stride: int, residual_scale: float, eps: float, h_out, out, out_type: int,
                           out_scales=None, stream=None) -> None:
-    _check(load_library().lens_op_sandwich_norm(_ptr(h), _ptr(y), y_type, M, D, rows_per_batch, _ptr(post_gain),
-                                                _ptr(gate), _ptr(pre_gain), _ptr(shift), _ptr(scale), mod_stride,
-                                                residual_scale, eps, _ptr(h_out), _ptr(out), out_type,
-                                                _ptr(out_scales), _stream(stream)), "lens_op_sandwich_norm")
+    """gate, shift and scale may be views into one modulation tensor (rows mod_stride apart)."""
+    ph, py, pp, pq, pho, po, pos, st = _whole("lens_op_sandwich_norm", stream, h, y, post_gain, pre_gain, h_out, out,
+                                              out_scales)
+    _check(load_library().lens_op_sandwich_norm(ph, py, y_type, M, D, rows_per_batch, pp, _ptr(gate), pq, _ptr(shift),
+                                                _ptr(scale), mod_stride, residual_scale, eps, pho, po, out_type, pos, st),
+           "lens_op_sandwich_norm")
 
 
 def lens_op_attention_window(q, k, v, B: int, heads: int, kv_heads: int, n_q: int, n_kv: int,
@@ -411,9 +439,10 @@ def lens_op_attention_window(q, k, v, B: int, heads: int, kv_heads: int, n_q: in
     kl = None if kv_len is None else array("i", kv_len)
     if (qs is not None and len(qs) != B) or (kl is not None and len(kl) != B):
         raise LensError(2, "lens_op_attention_window")
-    _check(load_library().lens_op_attention_window(_ptr(q), _ptr(k), _ptr(v), B, heads, kv_heads, n_q, n_kv,
-                                                   qs and qs.buffer_info()[0], kl and kl.buffer_info()[0], left, right, sinks, scale, _ptr(out),
-                                                   _stream(stream)), "lens_op_attention_window")
+    pq, pk, pv, po, st = _whole("lens_op_attention_window", stream, q, k, v, out)
+    _check(load_library().lens_op_attention_window(pq, pk, pv, B, heads, kv_heads, n_q, n_kv,
+                                                   qs and qs.buffer_info()[0], kl and kl.buffer_info()[0], left,
+                                                   right, sinks, scale, po, st), "lens_op_attention_window")
 
 
 def lens_op_euler_cfg(x, v_cond, v_uncond, n: int, dt: float, guidance: float, stream=None) -> None:

@@ -352,6 +352,8 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, cudaSt
 // Key tiles of 128 that no row of the CTA attends are never read: the walk goes through
 // the tiles of the sinks and then those of the window.  A key tile inside every row's
 // range takes no mask; in the others a thread turns its rows' ranges into one bit per score.
+// Up to 16 sinks in a tile of their own would cost a whole tile's work for a few keys: they
+// come last, as 16 keys (1999 queries, window 512, 4 sinks: 54.8 us for 59.2).
 // V rows of keys that no row of the CTA attends (padding, evicted tokens) become zeros in
 // shared memory: their weights are zero, but zero times what they hold need not be.
 // TMEM columns: S [0, 128), O [128, 192), P [192, 256).
@@ -378,11 +380,16 @@ struct Bars {
 static_assert(sizeof(Bars) <= 256, "barriers overflow their shared-memory reserve");
 
 // The CTA's walk over key tiles: j = 0 .. count-1 are the tiles [0, sinks) and then first,
-// first + 1, ...
+// first + 1, ...; with `few` (at most FEW sinks, the only keys of their tile) they are first,
+// first + 1, ... and then, from j = full, the sinks as a tile of FEW keys.
+constexpr int FEW = 16;
 struct Walk {
-  int count, sinks, first;
+  int count, full, sinks, first;
   int sink, lo, hi;            // keys any row attends: [0, sink) and [lo, hi)
-  __device__ __forceinline__ int key(int j) const { return (j < sinks ? j : first + (j - sinks)) * BKV; }
+  __device__ __forceinline__ bool few() const { return full < count; }
+  __device__ __forceinline__ int key(int j) const {
+    return (j >= full ? 0 : j < sinks ? j : first + (j - sinks)) * BKV;
+  }
   // whether the tile holds keys that no row of the CTA attends
   __device__ __forceinline__ bool dirty(int j) const {
     const int k = key(j);
@@ -400,7 +407,11 @@ __device__ __forceinline__ Walk walk_of(const WindowArgs& a, int start, int len,
   const int window = w.hi > w.lo ? (w.hi + BKV - 1) / BKV - w.first : 0;
   w.sinks = (w.sink + BKV - 1) / BKV;
   if (window > 0) w.sinks = min(w.sinks, w.first);
-  w.count = w.sinks + window;
+  w.count = w.full = w.sinks + window;
+  if (w.sinks == 1 && w.sink <= FEW) {
+    w.sinks = 0;
+    --w.full;
+  }
   return w;
 }
 
@@ -492,7 +503,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     } else if (warp == 1) {
       // -------------------------------------------------------------- S issuer
       if (lane == 0 && nkv > 0) {
-        constexpr uint32_t idesc_s = umma_idesc_bf16(128, BKV);
+        constexpr uint32_t idesc_s = umma_idesc_bf16(128, BKV), idesc_few = umma_idesc_bf16(128, FEW);
         bool ok = mbar_wait(&bar.q_full, 0, err);
         const uint64_t qdesc = umma_desc_sw128(smem_u32(sm));
         for (int j = 0; ok && j < nkv; ++j) {
@@ -503,7 +514,8 @@ __global__ void __launch_bounds__(THREADS, 2)
           tc_fence_after();
           const uint64_t kdesc = umma_desc_sw128(smem_u32(sKV + s * 2 * KV_BYTES));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_bf16(tmem, qdesc + 2 * k, kdesc + 2 * k, idesc_s, k > 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(tmem, qdesc + 2 * k, kdesc + 2 * k, j < walk.full ? idesc_s : idesc_few, k > 0 ? 1u : 0u);
           umma_commit(&bar.s_full);
           umma_commit(&bar.kv_empty[s]);
         }
@@ -527,9 +539,11 @@ __global__ void __launch_bounds__(THREADS, 2)
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 8; ++k) {
+            if (k * 16 >= FEW && j >= walk.full) break;
             umma_bf16_ts(tmem + O_COL, tmem + P_COL + 8 * k, umma_desc_sw128_mn(vbase + k * 2048), idesc_pv,
                          (j > 0 || k > 0) ? 1u : 0u);
+          }
           umma_commit(&bar.pv_done);
           umma_commit(&bar.kv_empty[s]);
         }
@@ -573,9 +587,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int all_s = ka.s, all_lo = kz.lo, all_hi = ka.hi;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     bool ok = true;
+    const int full = walk.full, first = walk.first - walk.sinks;
 #pragma unroll 2
-    for (int j = 0; j < nkv; ++j) {
-      const int key0 = walk.key(j);
+    for (int j = 0; j < full; ++j) {
+      const int key0 = (j < walk.sinks ? j : first + j) * BKV;
       if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full, j & 1, err))) {
         ok = false;
         break;
@@ -675,6 +690,72 @@ __global__ void __launch_bounds__(THREADS, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full);
     }
+    if (ok && walk.few()) {
+      // the sinks: the same on FEW keys, two columns of a thread's share each 8
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.s_full, full & 1, err));
+      if (ok) {
+        tc_fence_after();
+        float sc[8];
+        tmem_ld_16x256b_x2(lane_addr, sc);
+        tmem_ld_wait();
+        const uint32_t on0 = below(k0.hi - cq) & (~below(k0.lo - cq) | below(k0.s - cq));
+        const uint32_t on1 = below(k1.hi - cq) & (~below(k1.lo - cq) | below(k1.s - cq));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!(on0 & (1u << i))) sc[4 * (i / 2) + i % 2] = -INFINITY;
+          if (!(on1 & (1u << i))) sc[4 * (i / 2) + 2 + i % 2] = -INFINITY;
+        }
+        float mx0 = max3f(sc[0], sc[1], fmaxf(sc[4], sc[5])), mx1 = max3f(sc[2], sc[3], fmaxf(sc[6], sc[7]));
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2)) * a.scale_log2;
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2)) * a.scale_log2;
+        float c0 = 1.f, c1 = 1.f;
+        if (mx0 > m0 + kRescaleThreshold) {
+          c0 = ex2(m0 - mx0);
+          m0 = mx0;
+        }
+        if (mx1 > m1 + kRescaleThreshold) {
+          c1 = ex2(m1 - mx1);
+          m1 = mx1;
+        }
+        const float n0 = m0 == -INFINITY ? 0.f : -m0, n1 = m1 == -INFINITY ? 0.f : -m1;
+        uint32_t pk[4];
+        l0 *= c0;
+        l1 *= c1;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float e0 = ex2(fmaf(sc[4 * g], a.scale_log2, n0)), e1 = ex2(fmaf(sc[4 * g + 1], a.scale_log2, n0));
+          const float e2 = ex2(fmaf(sc[4 * g + 2], a.scale_log2, n1)), e3 = ex2(fmaf(sc[4 * g + 3], a.scale_log2, n1));
+          l0 += e0 + e1;
+          l1 += e2 + e3;
+          pk[2 * g] = pack_bf16x2(e0, e1);
+          pk[2 * g + 1] = pack_bf16x2(e2, e3);
+        }
+        ok = full == 0 || __all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (full - 1) & 1, err));
+        if (ok) {
+          tc_fence_after();
+          tmem_st_16x128b_x2(lane_addr + P_COL, pk);
+          if (full > 0 && __any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
+            float o[32];
+            tmem_ld_16x256b_x8(lane_addr + O_COL, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              o[4 * g] *= c0;
+              o[4 * g + 1] *= c0;
+              o[4 * g + 2] *= c1;
+              o[4 * g + 3] *= c1;
+            }
+            tmem_st_16x256b_x8(lane_addr + O_COL, o);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_full);
+        }
+      }
+    }
     // row sums: the four threads of a row hold disjoint keys
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -769,7 +850,7 @@ extern "C" lens_status lens_op_attention_window(const uint16_t* q, const uint16_
   if (!q || !k || !v || !out) return LENS_ERR_INVALID_ARG;
   if (B < 1 || B > kMaxRows || heads < 1 || heads > 1024 || kv_heads < 1 || heads % kv_heads) return LENS_ERR_SHAPE;
   if (n_q < 1 || n_q > kMaxPos || n_kv < 1 || n_kv > kMaxPos) return LENS_ERR_SHAPE;
-  if (!(scale > 0.f) || !isfinite(scale) || left < -1 || right < -1 || sinks < 0) return LENS_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale * 1.4426950408889634f) || left < -1 || right < -1 || sinks < 0) return LENS_ERR_INVALID_ARG;
   RowSpans spans;
   for (int b = 0; b < B; ++b) {
     spans.start[b] = q_start ? q_start[b] : 0;

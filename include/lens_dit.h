@@ -340,6 +340,10 @@ LENS_API lens_status lens_op_attention_masked(const uint16_t* q, const uint16_t*
                                               int n_txt, int n_img, const int* txt_len, uint16_t* out_txt,
                                               uint16_t* out_img, void* stream);
 
+/* The next four operations.  The first call of each on a device loads its kernels, so it
+ * belongs in set-up, before a stream capture; later calls can be captured.  They use no
+ * workspace: calls on different streams may overlap. */
+
 /* Element types of the operations below that take more than one. */
 typedef enum lens_dtype {
   LENS_F32 = 0,
@@ -408,11 +412,11 @@ LENS_API lens_status lens_op_sandwich_norm(const float* h, const void* y, lens_d
  *   q_start  host int [B], >= 0, or NULL (0);  kv_len host int [B], 0..n_kv, or NULL (n_kv)
  *   left, right  >= 0, or -1 for no bound on that side;  sinks >= 0
  * Keys that a query does not attend have no effect on its output, whatever K and V hold
- * there (a non-finite value inside the tile costs time).  n_q may be anything from one
+ * there (a non-finite value in V near attended keys costs time).  n_q may be anything from one
  * token against a long cache to all of them.  B <= 64; heads a multiple of kv_heads, at
  * most 1024; q, k, v, out 16-byte aligned; out must not overlap q, k or v.
- * Errors: INVALID_ARG (NULL, misaligned, scale not finite or <= 0, left or right < -1,
- * sinks < 0), SHAPE (B, heads, kv_heads, n_q, n_kv < 1, lengths or starts out of range,
+ * Errors: INVALID_ARG (NULL, misaligned, scale <= 0 or not finite times log2(e), left or
+ * right < -1, sinks < 0), SHAPE (B, heads, kv_heads, n_q, n_kv < 1, lengths or starts out of range,
  * q_start + n_q or n_kv > 2^29). */
 LENS_API lens_status lens_op_attention_window(const uint16_t* q, const uint16_t* k, const uint16_t* v, int B, int heads,
                                               int kv_heads, int n_q, int n_kv, const int* q_start, const int* kv_len,

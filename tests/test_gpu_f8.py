@@ -118,7 +118,8 @@ def check_gemm(c, codes_a, sa, codes_w, sw, bias, K, bf16):
 
 SIZES = [(1, 16, 16), (1, 4608, 1536), (2, 144, 400), (8, 1536, 4096), (9, 272, 1552), (16, 8192, 1536), (17, 128, 128),
          (33, 2000, 2880), (77, 1536, 4096), (128, 256, 384), (129, 400, 144), (255, 512, 1536), (333, 4608, 1536),
-         (513, 1040, 2896), (1152, 1536, 1536), (4352, 1536, 4096)]
+         (513, 1040, 2896), (1152, 1536, 1536), (4352, 1536, 4096),
+         (40, 16, 16), (300, 16, 272), (64, 1536, 2576), (200, 400, 11520), (1500, 8192, 400), (2100, 4624, 144)]
 
 
 @pytest.mark.parametrize("bf16", [False, True])
@@ -190,3 +191,11 @@ def test_gemm_f8_large_outputs_pass_32_bit_offsets():
     L.lens_op_gemm_f8(ca, sa, cw, sw, None, c, L.LENS_BF16, M, N, K)
     torch.cuda.synchronize()
     assert bool((c[-1] == 16).all()) and bool((c[-2] == 2).all()) and not bool(c[:-2].any())
+
+
+def test_refuses_views_that_are_not_contiguous():
+    x = torch.zeros((64, 256), device="cuda")
+    codes, scales = torch.zeros((64, 128), dtype=torch.uint8, device="cuda"), torch.zeros((1, 64), device="cuda")
+    with pytest.raises(L.LensError) as ei:
+        L.lens_op_quantize_f8(x[:, :128], L.LENS_F32, 64, 128, 1, codes, scales)
+    assert ei.value.status == 1

@@ -85,7 +85,7 @@ def tolerances(t, h, out, branch, opt, residual_scale=RS):
 @pytest.mark.parametrize("M,D,rpb,use,y_bf16", [
     (1, 16, 1, (), True), (3, 144, 2, ALL, True), (77, 1536, 77, ("post_gain", "gate"), True),
     (130, 1536, 65, ALL, False), (9, 2896, 4, ("pre_gain", "shift"), True), (5, 4096, 100, ("scale",), False),
-    (33, 4112, 11, ALL, True), (7, 8192, 3, ALL, True), (2, 8192, 1, ("gate",), False), (1000, 272, 333, ALL, True)])
+    (33, 4112, 11, ALL, True), (3001, 128, 7, ALL, True), (700, 2048, 699, ALL, False), (7, 8192, 3, ALL, True), (2, 8192, 1, ("gate",), False), (1000, 272, 333, ALL, True)])
 def test_sandwich_norm(M, D, rpb, use, y_bf16):
     t = make(M, D, rpb, M + D, y_bf16)
     h, out, branch, opt = reference(t, M, rpb, use)

@@ -62,7 +62,7 @@ def test_attention_window_refusals(lib):
         return lib.lens_op_attention_window(P(q), P(k), P(v), b, h, hk, nq, nkv, ints(start), ints(length), left, right,
                                             sinks, scale, P(out), None)
     for kw in (dict(q=0), dict(k=0), dict(v=0), dict(out=0), dict(q=8), dict(k=8), dict(v=8), dict(out=8),
-               dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(left=-2),
+               dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(left=-2),
                dict(right=-2), dict(sinks=-1)):
         assert call(**kw) == BAD, kw
     for kw in (dict(b=0), dict(b=65), dict(h=0), dict(h=1025, hk=1025), dict(hk=0), dict(h=4, hk=3), dict(nq=0),
@@ -75,3 +75,18 @@ def test_binding_refuses_lengths_for_another_batch():
     with pytest.raises(binding.LensError) as ei:
         binding.lens_op_attention_window(None, None, None, 2, 4, 4, 1, 8, [0], [8, 8], 1, 0, 0, 0.125, None, stream=0)
     assert ei.value.status == SHAPE
+
+
+def test_binding_refuses_host_tensors():
+    """Tensors that are not on the current device (here: on the host) never reach the library."""
+    import torch
+    f, b = torch.zeros(128, 128), torch.zeros(128, 128, dtype=torch.uint8)
+    for call in (lambda: binding.lens_op_quantize_f8(f, 0, 128, 128, 1, b, f, stream=0),
+                 lambda: binding.lens_op_gemm_f8(b, f, b, f, None, f, 0, 128, 128, 128, stream=0),
+                 lambda: binding.lens_op_sandwich_norm(f, f, 0, 128, 128, 1, None, None, None, None, None, 0, 1.0, 1e-6,
+                                                       f, f, 1, stream=0),
+                 lambda: binding.lens_op_attention_window(f, f, f, 1, 1, 1, 1, 1, None, None, 0, 0, 0, 0.125, f,
+                                                          stream=0)):
+        with pytest.raises(binding.LensError) as ei:
+            call()
+        assert ei.value.status == BAD
