@@ -143,99 +143,100 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   uint32_t prod_issued = 0;
   bool prod_ok = true;
-  // 128 sums and 64 loaded columns a thread do not fit an even share of the registers: the
-  // epilogue's two warpgroups take over what the first gives up (72 + 2 x 216 = 3 x 168)
+  // HALVES = 2: 128 sums and 64 loaded columns a thread do not fit an even share of the
+  // registers, so the epilogue's two warpgroups take over what the first gives up (72 + 2 x
+  // 216 = 3 x 168)
   if (warp < 4) {
-  if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
-      for (int t = pair; t < a.total_tiles && prod_ok; t += npairs) {
-        const int tn = t / a.tiles_m, m0 = (t - tn * a.tiles_m) * 256 + 128 * (int)rank, n0 = tn * BN + (BN / 2) * (int)rank;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, a.err)) {
-            prod_ok = false;
+    if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      if (lane == 0) {
+        uint32_t stage = 0, phase = 0;
+        for (int t = pair; t < a.total_tiles && prod_ok; t += npairs) {
+          const int tn = t / a.tiles_m, m0 = (t - tn * a.tiles_m) * 256 + 128 * (int)rank, n0 = tn * BN + (BN / 2) * (int)rank;
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1, a.err)) {
+              prod_ok = false;
+              break;
+            }
+            if (rank == 0) mbar_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+            tma_load_2d_pair(sA + stage * C::A_BYTES, &tmA, &full[stage], kb * 128, m0);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h)
+              tma_load_2d_pair(sW + stage * C::B_BYTES + h * C::HALF_BYTES, &tmW, &full[stage], kb * 128, n0 + 64 * h);
+            ++prod_issued;
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        // the leader reconciles both CTAs' loads if the pair aborts
+        if (rank == 1) st_shared_cluster_u32(mapa_shared(smem_u32(peer_issued), base), prod_issued);
+      }
+      __syncwarp();
+    } else if (warp == 1 || warp == 2) {
+      if (lane == 0 && rank == 0) {
+        constexpr uint32_t idesc = umma_idesc_e4m3(256, BN);
+        const uint32_t odd = warp == 2;
+        bool ok = true;
+        uint32_t stage = odd, phase = 0, slot = odd, use = 0;
+        const int64_t blocks = (int64_t)((a.total_tiles - pair + npairs - 1) / npairs) * (kb1 - kb0);
+        for (int64_t i = odd; i < blocks; i += 2) {
+          if (!mbar_wait_sleep(&tempty[slot], use ^ 1, a.err) || !mbar_wait_sleep(&full[stage], phase, a.err)) {
+            ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
-          tma_load_2d_pair(sA + stage * C::A_BYTES, &tmA, &full[stage], kb * 128, m0);
+          tc_fence_after();
+          const uint64_t ad = umma_desc_sw128(smem_u32(sA + stage * C::A_BYTES));
+          const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * C::B_BYTES));
 #pragma unroll
-          for (int h = 0; h < HALVES; ++h)
-            tma_load_2d_pair(sW + stage * C::B_BYTES + h * C::HALF_BYTES, &tmW, &full[stage], kb * 128, n0 + 64 * h);
-          ++prod_issued;
-          if (++stage == STAGES) {
-            stage = 0;
+          for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + slot * BN, ad + 2 * k, wd + 2 * k, idesc, k > 0 ? 1u : 0u);
+          umma_commit_pair(&empty[stage], both);
+          umma_commit_pair(&tfull[slot], both);
+          if ((stage += 2) >= STAGES) {
+            stage -= STAGES;
             phase ^= 1;
+          }
+          if ((slot += 2) >= SLOTS) {
+            slot -= SLOTS;
+            use ^= 1;
+          }
+        }
+        if (!ok) umma_drain_pair(&drain[odd], (uint16_t)(1u << base));
+      }
+      __syncwarp();
+    } else {
+      uint32_t slot = 0, use = 0;
+      bool ok = true;
+      for (int t = pair; t < a.total_tiles && ok; t += npairs) {
+        const int tn = t / a.tiles_m, row = (t - tn * a.tiles_m) * 256 + 128 * (int)rank + lane;
+        const float* pa = a.as + (int64_t)kb0 * a.M + row;
+        // a column block past the last one holds no output: any block's scale will do
+        const float* pw = a.ws + (int64_t)kb0 * a.nblocks + min(tn * HALVES + (lane & (HALVES - 1)), a.nblocks - 1);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&sfree[slot], use ^ 1, a.err))) {
+            ok = false;
+            break;
+          }
+          float* dst = sScale + slot * SCALES;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool live = row + 32 * i < a.M;
+            cp_async4(dst + lane + 32 * i, live ? pa + 32 * i : a.as, live);
+          }
+          if (lane < HALVES) cp_async4(dst + 128 + lane, pw, true);
+          cp_async_arrive(&tfull[slot]);
+          pa += a.M;
+          pw += a.nblocks;
+          if (++slot == SLOTS) {
+            slot = 0;
+            use ^= 1;
           }
         }
       }
-      // the leader reconciles both CTAs' loads if the pair aborts
-      if (rank == 1) st_shared_cluster_u32(mapa_shared(smem_u32(peer_issued), base), prod_issued);
+      cp_async_wait_all();
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp == 1 || warp == 2) {
-    if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = umma_idesc_e4m3(256, BN);
-      const uint32_t odd = warp == 2;
-      bool ok = true;
-      uint32_t stage = odd, phase = 0, slot = odd, use = 0;
-      const int64_t blocks = (int64_t)((a.total_tiles - pair + npairs - 1) / npairs) * (kb1 - kb0);
-      for (int64_t i = odd; i < blocks; i += 2) {
-        if (!mbar_wait_sleep(&tempty[slot], use ^ 1, a.err) || !mbar_wait_sleep(&full[stage], phase, a.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t ad = umma_desc_sw128(smem_u32(sA + stage * C::A_BYTES));
-        const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * C::B_BYTES));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + slot * BN, ad + 2 * k, wd + 2 * k, idesc, k > 0 ? 1u : 0u);
-        umma_commit_pair(&empty[stage], both);
-        umma_commit_pair(&tfull[slot], both);
-        if ((stage += 2) >= STAGES) {
-          stage -= STAGES;
-          phase ^= 1;
-        }
-        if ((slot += 2) >= SLOTS) {
-          slot -= SLOTS;
-          use ^= 1;
-        }
-      }
-      if (!ok) umma_drain_pair(&drain[odd], (uint16_t)(1u << base));
-    }
-    __syncwarp();
-  } else {
-    uint32_t slot = 0, use = 0;
-    bool ok = true;
-    for (int t = pair; t < a.total_tiles && ok; t += npairs) {
-      const int tn = t / a.tiles_m, row = (t - tn * a.tiles_m) * 256 + 128 * (int)rank + lane;
-      const float* pa = a.as + (int64_t)kb0 * a.M + row;
-      // a column block past the last one holds no output: any block's scale will do
-      const float* pw = a.ws + (int64_t)kb0 * a.nblocks + min(tn * HALVES + (lane & (HALVES - 1)), a.nblocks - 1);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sfree[slot], use ^ 1, a.err))) {
-          ok = false;
-          break;
-        }
-        float* dst = sScale + slot * SCALES;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool live = row + 32 * i < a.M;
-          cp_async4(dst + lane + 32 * i, live ? pa + 32 * i : a.as, live);
-        }
-        if (lane < HALVES) cp_async4(dst + 128 + lane, pw, true);
-        cp_async_arrive(&tfull[slot]);
-        pa += a.M;
-        pw += a.nblocks;
-        if (++slot == SLOTS) {
-          slot = 0;
-          use ^= 1;
-        }
-      }
-    }
-    cp_async_wait_all();
-    __syncwarp();
-  }
   } else {
     if constexpr (HALVES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3, part = (warp - 4) >> 2;
