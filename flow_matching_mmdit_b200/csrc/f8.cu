@@ -95,8 +95,8 @@ cudaError_t launch_quantize_f8(const void* x, bool bf16, int64_t rows, int64_t k
                       rows, k, codes, scales);
   }
   const dim3 grid((unsigned)((rows + kF8Group - 1) / kF8Group), groups);
-  return launch_pdl(bf16 ? quantize_f8_blocks_kernel<true> : quantize_f8_blocks_kernel<false>, grid, dim3(512), 0, st, x,
-                    rows, k, codes, scales);
+  return launch_pdl(bf16 ? quantize_f8_blocks_kernel<true> : quantize_f8_blocks_kernel<false>, grid, dim3(512), 0, st,
+                    x, rows, k, codes, scales);
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

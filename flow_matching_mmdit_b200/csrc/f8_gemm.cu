@@ -76,10 +76,21 @@ __device__ __forceinline__ float4 ld_cluster4(const float4* p, uint32_t rank) {
 
 struct F8GemmArgs {
   void* C;
-  int M, N, kblocks, tiles_m, total_tiles, nblocks;
+  int M, N, kblocks, tiles_m, tiles_n, total_tiles, nblocks;
   const float *as, *ws, *bias;
   int* err;
 };
+
+// Tile t: columns of tiles within bands of BAND rows of them, so that the pairs at work at one
+// time share few rows of A and few of W (2 % at 8704 x 1536 x 4096 over whole columns; 4 and
+// 16 rows measure the same).
+constexpr int BAND = 8;
+__device__ __forceinline__ void tile_of(const F8GemmArgs& a, int t, int& tm, int& tn) {
+  const int band = t / (BAND * a.tiles_n), first = band * BAND, rows = min(BAND, a.tiles_m - first);
+  const int l = t - first * a.tiles_n;
+  tn = l / rows;
+  tm = first + l - tn * rows;
+}
 
 template <int HALVES, bool BF16, int SPLITS>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -152,7 +163,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) {
         uint32_t stage = 0, phase = 0;
         for (int t = pair; t < a.total_tiles && prod_ok; t += npairs) {
-          const int tn = t / a.tiles_m, m0 = (t - tn * a.tiles_m) * 256 + 128 * (int)rank, n0 = tn * BN + (BN / 2) * (int)rank;
+          int tm, tn;
+        tile_of(a, t, tm, tn);
+        const int m0 = tm * 256 + 128 * (int)rank, n0 = tn * BN + (BN / 2) * (int)rank;
           for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1, a.err)) {
               prod_ok = false;
@@ -209,7 +222,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t slot = 0, use = 0;
       bool ok = true;
       for (int t = pair; t < a.total_tiles && ok; t += npairs) {
-        const int tn = t / a.tiles_m, row = (t - tn * a.tiles_m) * 256 + 128 * (int)rank + lane;
+        int tm, tn;
+      tile_of(a, t, tm, tn);
+      const int row = tm * 256 + 128 * (int)rank + lane;
         const float* pa = a.as + (int64_t)kb0 * a.M + row;
         // a column block past the last one holds no output: any block's scale will do
         const float* pw = a.ws + (int64_t)kb0 * a.nblocks + min(tn * HALVES + (lane & (HALVES - 1)), a.nblocks - 1);
@@ -293,7 +308,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) break;
-      const int tn = t / a.tiles_m, row0 = (t - tn * a.tiles_m) * 256 + 128 * (int)rank + quarter * 32;
+      int tm, tn;
+      tile_of(a, t, tm, tn);
+      const int row0 = tm * 256 + 128 * (int)rank + quarter * 32;
       const int n0 = tn * BN + part * COLS;
       if constexpr (SPLIT) {
         // this pair's part of the sum, [part][16-byte piece of the columns][row]; the stages
@@ -342,8 +359,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   if constexpr (SPLIT) {
     // each of the cluster's pairs finishes a share of the columns, adding the pairs' parts in order
     if (warp >= 4 && !err_raised(a.err)) {
-      const int quarter = warp & 3, part = (warp - 4) >> 2, tn = pair / a.tiles_m;
-      const int row = (pair - tn * a.tiles_m) * 256 + 128 * (int)rank + quarter * 32 + lane;
+      const int quarter = warp & 3, part = (warp - 4) >> 2;
+      int tm, tn;
+      tile_of(a, pair, tm, tn);
+      const int row = tm * 256 + 128 * (int)rank + quarter * 32 + lane;
       constexpr int SHARE = 16 / SPLITS;
       const int first = SHARE * (int)(base >> 1);
       const float4* mine = reinterpret_cast<const float4*>(smem) + part * 16 * 128 + quarter * 32 + lane;
@@ -399,7 +418,8 @@ cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
   a.kblocks = (g.K + kF8Group - 1) / kF8Group;
   a.nblocks = (g.N + kF8Group - 1) / kF8Group;
   a.tiles_m = (g.M + 255) / 256;
-  a.total_tiles = a.tiles_m * ((g.N + C::BN - 1) / C::BN);
+  a.tiles_n = (g.N + C::BN - 1) / C::BN;
+  a.total_tiles = a.tiles_m * a.tiles_n;
   a.as = g.a_scales;
   a.ws = g.w_scales;
   a.bias = g.bias;

@@ -88,7 +88,8 @@ struct Branch8<true> {
 __device__ __forceinline__ float inv_rms(float sum, int D, float eps) { return __frsqrt_rn(sum / D + eps); }
 
 template <int THREADS, bool Y_BF16, bool OUT_F8>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) sandwich_norm_kernel(const __grid_constant__ SandwichArgs a) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    sandwich_norm_kernel(const __grid_constant__ SandwichArgs a) {
   __shared__ __align__(16) float red[2][32];
   const int col = 8 * threadIdx.x;
   const bool on = col < a.D;
@@ -209,6 +210,7 @@ extern "C" lens_status lens_op_sandwich_norm(const float* h, const void* y, lens
   const bool yb = y_type == LENS_BF16, of8 = out_type == LENS_F8E4M3;
   const int sms = device_sms();
   const cudaError_t e = yb ? (of8 ? launch_sandwich<true, true>(a, sms, st) : launch_sandwich<true, false>(a, sms, st))
-                           : (of8 ? launch_sandwich<false, true>(a, sms, st) : launch_sandwich<false, false>(a, sms, st));
+                           : (of8 ? launch_sandwich<false, true>(a, sms, st)
+                                  : launch_sandwich<false, false>(a, sms, st));
   return e == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
 }

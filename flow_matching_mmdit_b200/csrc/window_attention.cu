@@ -97,7 +97,9 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "f"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <int SPLITS, int WARPS>
@@ -211,7 +213,10 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
                              pack_bf16x2(s[2 * t + 1][2], s[2 * t + 1][3])};
       uint32_t w[4][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e][0] = vr[t][e].x, w[e][1] = vr[t][e].y, w[e][2] = vr[t][e].z, w[e][3] = vr[t][e].w;
+      for (int e = 0; e < 4; ++e) {
+        w[e][0] = vr[t][e].x, w[e][1] = vr[t][e].y;
+        w[e][2] = vr[t][e].z, w[e][3] = vr[t][e].w;
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
@@ -850,7 +855,8 @@ extern "C" lens_status lens_op_attention_window(const uint16_t* q, const uint16_
   if (!q || !k || !v || !out) return LENS_ERR_INVALID_ARG;
   if (B < 1 || B > kMaxRows || heads < 1 || heads > 1024 || kv_heads < 1 || heads % kv_heads) return LENS_ERR_SHAPE;
   if (n_q < 1 || n_q > kMaxPos || n_kv < 1 || n_kv > kMaxPos) return LENS_ERR_SHAPE;
-  if (!(scale > 0.f) || !isfinite(scale * 1.4426950408889634f) || left < -1 || right < -1 || sinks < 0) return LENS_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale * 1.4426950408889634f) || left < -1 || right < -1 || sinks < 0)
+    return LENS_ERR_INVALID_ARG;
   RowSpans spans;
   for (int b = 0; b < B; ++b) {
     spans.start[b] = q_start ? q_start[b] : 0;
