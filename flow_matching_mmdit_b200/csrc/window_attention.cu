@@ -447,6 +447,13 @@ __global__ void __launch_bounds__(THREADS, 2)
   const Walk walk = walk_of(a, start, len, q0);
   const int nkv = walk.count;
 
+  const int bhk = b * a.kv_heads + h / (a.heads / a.kv_heads);
+  auto load_kv = [&](int j) {
+    const int s = j % STAGES;
+    mbar_expect_tx(&bar.kv_full[s], 2 * KV_BYTES);
+    tma_load_3d(sKV + s * 2 * KV_BYTES, &tmK, &bar.kv_full[s], 0, walk.key(j), bhk);
+    tma_load_3d(sKV + s * 2 * KV_BYTES + KV_BYTES, &tmV, &bar.kv_full[s], 0, walk.key(j), bhk);
+  };
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 1);
     for (int s = 0; s < STAGES; ++s) {
@@ -461,9 +468,13 @@ __global__ void __launch_bounds__(THREADS, 2)
     mbar_init(&bar.drain[0], 1);
     mbar_init(&bar.drain[1], 1);
     fence_mbar_init();
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    // this thread is the producer too: its first loads need nobody else's set-up
+    grid_dependency_wait();
+    if (nkv > 0) {
+      mbar_expect_tx(&bar.q_full, Q_BYTES);
+      tma_load_3d(sm, &tmQ, &bar.q_full, 0, q0, b * a.heads + h);
+      for (int j = 0; j < min(nkv, STAGES); ++j) load_kv(j);
+    }
   }
   if (warp == 1) {
     tmem_alloc(&bar.tmem_slot, 256);
@@ -482,20 +493,14 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (warp == 0) {
       // -------------------------------------------------------------- TMA producer
       if (lane == 0 && nkv > 0) {
-        int issued = 0;
+        int issued = min(nkv, STAGES);          // the first ones above
         bool ok = true;
-        const int bh = b * a.heads + h, bhk = b * a.kv_heads + h / (a.heads / a.kv_heads);
-        mbar_expect_tx(&bar.q_full, Q_BYTES);
-        tma_load_3d(sm, &tmQ, &bar.q_full, 0, q0, bh);
-        for (int j = 0; j < nkv; ++j) {
-          const int s = j % STAGES;
-          if (!mbar_wait(&bar.kv_empty[s], ((j / STAGES) & 1) ^ 1, err)) {
+        for (int j = issued; j < nkv; ++j) {
+          if (!mbar_wait(&bar.kv_empty[j % STAGES], ((j / STAGES) & 1) ^ 1, err)) {
             ok = false;
             break;
           }
-          mbar_expect_tx(&bar.kv_full[s], 2 * KV_BYTES);
-          tma_load_3d(sKV + s * 2 * KV_BYTES, &tmK, &bar.kv_full[s], 0, walk.key(j), bhk);
-          tma_load_3d(sKV + s * 2 * KV_BYTES + KV_BYTES, &tmV, &bar.kv_full[s], 0, walk.key(j), bhk);
+          load_kv(j);
           issued = j + 1;
         }
         mbar_wait_drain(&bar.q_full, 0);
@@ -777,26 +782,35 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int i = 0; i < 32; ++i) o[i] = 0.f;
       }
       uint32_t redo = 0;     // rows of this warp that came out non-finite
+      // the warp's sixteen rows go out through its own rows of Q's place (every S has been
+      // computed), so that a row leaves in 16-byte pieces; chunk c of row r at c ^ (r % 8)
+      uint8_t* stage = sm + wrow * 128;
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
-        const int tok = q0 + rlo + 8 * rr;
+        const int r = (lane >> 2) + 8 * rr;
         // a row with no attended key (l = 0) writes zeros rather than 0 * inf
         const float lr = rr ? l1 : l0;
         const float inv = lr > 0.f ? 1.f / lr : 0.f;
         float bad = lr * 0.f;                              // 0, or NaN
 #pragma unroll
-        for (int g = 0; g < 8; ++g) bad += (o[4 * g + 2 * rr] + o[4 * g + 2 * rr + 1]) * 0.f;
-        if (tok < a.n_q) {
-          uint32_t* d32 = reinterpret_cast<uint32_t*>(a.out + (((int64_t)b * a.n_q + tok) * a.heads + h) * 64 + cq);
-#pragma unroll
-          for (int g = 0; g < 8; ++g)
-            d32[4 * g] = lr == 0.f ? 0u : pack_bf16x2(o[4 * g + 2 * rr] * inv, o[4 * g + 2 * rr + 1] * inv);
+        for (int g = 0; g < 8; ++g) {
+          bad += (o[4 * g + 2 * rr] + o[4 * g + 2 * rr + 1]) * 0.f;
+          *reinterpret_cast<uint32_t*>(stage + r * 128 + ((g ^ (r & 7)) << 4) + 2 * cq) =
+              lr == 0.f ? 0u : pack_bf16x2(o[4 * g + 2 * rr] * inv, o[4 * g + 2 * rr + 1] * inv);
         }
-        uint32_t v = __ballot_sync(0xffffffffu, bad != 0.f && tok < a.n_q);
+        uint32_t v = __ballot_sync(0xffffffffu, bad != 0.f && q0 + wrow + r < a.n_q);
         v |= v >> 1;
         v |= v >> 2;                                       // bit 4 r: row r's four threads
 #pragma unroll
-        for (int r = 0; r < 8; ++r) redo |= ((v >> (4 * r)) & 1u) << (r + 8 * rr);
+        for (int i = 0; i < 8; ++i) redo |= ((v >> (4 * i)) & 1u) << (i + 8 * rr);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 3) + 4 * i, c = lane & 7, tok = q0 + wrow + r;
+        if (tok < a.n_q)
+          reinterpret_cast<uint4*>(a.out + (((int64_t)b * a.n_q + tok) * a.heads + h) * 64)[c] =
+              *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
       }
       // A non-finite value in V reaches the whole tile through a weight of zero: such rows
       // are done again from their attended keys alone.
