@@ -312,14 +312,20 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
       attend_row(a, b, hk * group + (row0 + r) % group, (row0 + r) / group, start + (row0 + r) / group, len);
 }
 
-cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, cudaStream_t st) {
+cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, int sms, cudaStream_t st) {
   const int rows = a.n_q * (a.heads / a.kv_heads);
-  // the most keys a tile may read decide how many CTAs share it (never the batch, so a
-  // row's result does not depend on what runs beside it)
+  // the most keys a tile may read
   const int64_t most = (int64_t)a.left + a.right + 16 + a.sinks;
   const int64_t keys = most < a.n_kv ? most : a.n_kv;
+  // A tile is shared by as many CTAs as have a step for each of four warps, as long as all
+  // CTAs run at once (three to an SM) or each warp has 16 steps to make up for their start and
+  // join.  1028 keys, us for 8 / 4 / 2 / 1 CTAs: 32 tiles 6.4 / 7.1 / 9.6 / 14, 96 tiles 14.8 /
+  // 10.8 / 11.8 / 15, 512 tiles 63 / 46 / 37 / 32.
+  const int64_t tiles = (int64_t)((rows + 15) / 16) * a.kv_heads * B;
   int splits = 1;
-  while (splits < kFewMaxSplit && splits * 4 * kFewStep < keys) splits *= 2;
+  while (splits < kFewMaxSplit && splits * 4 * kFewStep < keys &&
+         (tiles * splits * 2 <= 3 * sms || keys >= (int64_t)splits * 2 * 4 * kFewStep * 16))
+    splits *= 2;
   // past two steps a warp: eight warps a CTA (8192 keys, 32 heads on 8: 10.2 us for 15.5;
   // 1028 keys: 15.5 for 8.0, fewer CTAs fit an SM)
   const bool wide = splits == kFewMaxSplit && keys > 2 * kFewMaxSplit * 4 * kFewStep;
@@ -847,7 +853,7 @@ cudaError_t launch_many(const WindowArgs& a, const RowSpans& spans, int B, int* 
 }
 
 // Rows are few where 16-row tiles are hardly more than 128-row ones (per key head; both
-// read the same keys), whatever the batch, so that a row's result does not depend on it.
+// read the same keys).
 // Over 1028 of 4352 keys, us for 16-row tiles (128-row tiles): 24 key heads, 1 query 7.0
 // (14.0), 16 queries 7.3 (15.5), 32 queries 8.4 (15.9); 4 sequences, 24 heads on 8 key heads,
 // 1 query 8.0 (16.2), 16 queries 15.6 (16.2), 32 queries 30 (16.2).
@@ -886,7 +892,7 @@ extern "C" lens_status lens_op_attention_window(const uint16_t* q, const uint16_
                      n_q, n_kv, left < 0 || left > kMaxPos ? kMaxPos : left,
                      right < 0 || right > kMaxPos ? kMaxPos : right, sinks, scale * 1.4426950408889634f};
   cudaStream_t st = (cudaStream_t)stream;
-  if (few_rows(a)) return launch_few(a, spans, B, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
+  if (few_rows(a)) return launch_few(a, spans, B, device_sms(), st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
   int* err = op_err_ptr();
   if (!err) return LENS_ERR_CUDA;
   return launch_many(a, spans, B, err, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;

@@ -358,7 +358,7 @@ typedef enum lens_dtype {
  *   x          dev [rows, k], fp32 or bf16 (x_type), 16-byte aligned; k a multiple of 16
  *   block_rows 1: a scale per row and 128 columns (activations); 128: a scale per
  *              128 x 128 (weights).  The last blocks may be partial.
- *   codes      dev uint8 [rows, k], 16-byte aligned
+ *   codes      dev uint8 [rows, k], 16-byte aligned, not overlapping x
  *   scales     dev fp32 [ceil(k / 128), ceil(rows / block_rows)]: block (r, g) at [g][r]
  * Errors: INVALID_ARG (NULL, misaligned, x_type, block_rows), SHAPE (rows < 1 or > 2^30,
  * k < 16, k % 16, k > 2^22). */
@@ -371,7 +371,8 @@ LENS_API lens_status lens_op_quantize_f8(const void* x, lens_dtype x_type, int64
  * on the 8-bit tensor cores, each 128-wide block accumulated in fp32, scaled and added
  * in fp32.
  *   A dev e4m3 [M, K], W dev e4m3 [N, K], bias dev fp32 [N] or NULL,
- *   C dev [M, N], fp32 or bf16 (c_type, rounded once).  A, W, C 16-byte aligned.
+ *   C dev [M, N], fp32 or bf16 (c_type, rounded once).  A, W, C 16-byte aligned, C overlapping
+ *   none of the inputs.
  * Errors: INVALID_ARG (NULL, misaligned, c_type), SHAPE (M, N or K < 1, N or K not a
  * multiple of 16, a size > 2^22). */
 LENS_API lens_status lens_op_gemm_f8(const uint8_t* A, const float* a_scales, const uint8_t* W, const float* w_scales,
@@ -412,8 +413,10 @@ LENS_API lens_status lens_op_sandwich_norm(const float* h, const void* y, lens_d
  *   q_start  host int [B], >= 0, or NULL (0);  kv_len host int [B], 0..n_kv, or NULL (n_kv)
  *   left, right  >= 0, or -1 for no bound on that side;  sinks >= 0
  * Keys that a query does not attend have no effect on its output, whatever K and V hold
- * there (a non-finite value in V near attended keys costs time).  n_q may be anything from one
- * token against a long cache to all of them.  B <= 64; heads a multiple of kv_heads, at
+ * there (rows near a non-finite value in V take longer and round differently).  n_q may be anything from one
+ * token against a long cache to all of them.  (For few queries the keys are split over more
+ * CTAs in a small batch than in a large one, so the last bit of a row may depend on the
+ * batch; for many it does not.)  B <= 64; heads a multiple of kv_heads, at
  * most 1024; q, k, v, out 16-byte aligned; out must not overlap q, k or v.
  * Errors: INVALID_ARG (NULL, misaligned, scale <= 0 or not finite times log2(e), left or
  * right < -1, sinks < 0), SHAPE (B, heads, kv_heads, n_q, n_kv < 1, lengths or starts out of range,

@@ -109,6 +109,17 @@ def test_few_queries_against_a_cache(H, Hk, nq, nkv, left, sinks):
     check(run(q, k, v, start, length, left, 0, sinks), q, k, v, start, length, left, 0, sinks)
 
 
+@pytest.mark.parametrize("B,H,Hk,nkv", [(40, 24, 24, 700), (64, 8, 8, 1100), (20, 16, 4, 2300)])
+def test_one_query_in_large_batches(B, H, Hk, nkv):
+    """Enough tiles for the keys to be split over fewer CTAs, down to one."""
+    g = np.random.default_rng(B)
+    length = [int(g.integers(0, nkv + 1)) for _ in range(B)]
+    start = [max(0, n - 1) for n in length]
+    q, k, v = make(B, H, Hk, 1, nkv, B)
+    for left in (-1, 500, 100):
+        check(run(q, k, v, start, length, left, 0, 4), q, k, v, start, length, left, 0, 4, heads=[0, H - 1])
+
+
 @pytest.mark.parametrize("nq", [1, 7, 300])
 @pytest.mark.parametrize("what", [float("nan"), float("inf"), -3e38])
 def test_values_in_places_that_are_not_attended_have_no_effect(nq, what):
@@ -164,6 +175,7 @@ def test_large_scores(nq):
 
 @pytest.mark.parametrize("nq,nkv", [(1, 2000), (300, 300)])
 def test_rows_do_not_depend_on_the_batch_streams_or_graphs(nq, nkv):
+    # (for few queries: while the batch leaves the split of the keys as it is)
     B, left, sinks = 3, 70, 4
     q, k, v = make(B, 6, 2, nq, nkv, 14)
     length = [nkv, nkv - 3, nkv // 2]
