@@ -853,13 +853,15 @@ cudaError_t launch_many(const WindowArgs& a, const RowSpans& spans, int B, int* 
 }
 
 // Rows are few where 16-row tiles are hardly more than 128-row ones (per key head; both
-// read the same keys).
-// Over 1028 of 4352 keys, us for 16-row tiles (128-row tiles): 24 key heads, 1 query 7.0
-// (14.0), 16 queries 7.3 (15.5), 32 queries 8.4 (15.9); 4 sequences, 24 heads on 8 key heads,
-// 1 query 8.0 (16.2), 16 queries 15.6 (16.2), 32 queries 30 (16.2).
-bool few_rows(const WindowArgs& a) {
+// read the same keys), or up to three times as many but so few in all that their keys can be
+// split.  Over 1028 of 4352 keys, us for 16-row tiles (128-row tiles): 24 heads on as many key
+// heads, 1 query 6.2 (14.0), 32 queries 8.4 (15.9), 48 queries 10.9 (14.6), 4 sequences of 48
+// 21.6 (16.8); 24 heads on 8 key heads, 48 queries 10.8 (14.7), 4 sequences of 16 10.8 (16.2),
+// of 32 17.0 (15.1), 16 of 32 43 (35).
+bool few_rows(const WindowArgs& a, int B, int sms) {
   const int64_t group = a.heads / a.kv_heads;
-  return (a.n_q * group + 15) / 16 <= group * ((a.n_q + tc::BQ - 1) / tc::BQ) + 1;
+  const int64_t small = (a.n_q * group + 15) / 16, large = group * ((a.n_q + tc::BQ - 1) / tc::BQ);
+  return small <= large + 1 || (small <= 3 * large && 2 * small * a.kv_heads * B <= sms);
 }
 
 }  // namespace
@@ -892,7 +894,8 @@ extern "C" lens_status lens_op_attention_window(const uint16_t* q, const uint16_
                      n_q, n_kv, left < 0 || left > kMaxPos ? kMaxPos : left,
                      right < 0 || right > kMaxPos ? kMaxPos : right, sinks, scale * 1.4426950408889634f};
   cudaStream_t st = (cudaStream_t)stream;
-  if (few_rows(a)) return launch_few(a, spans, B, device_sms(), st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
+  const int sms = device_sms();
+  if (few_rows(a, B, sms)) return launch_few(a, spans, B, sms, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
   int* err = op_err_ptr();
   if (!err) return LENS_ERR_CUDA;
   return launch_many(a, spans, B, err, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;

@@ -414,9 +414,9 @@ LENS_API lens_status lens_op_sandwich_norm(const float* h, const void* y, lens_d
  *   left, right  >= 0, or -1 for no bound on that side;  sinks >= 0
  * Keys that a query does not attend have no effect on its output, whatever K and V hold
  * there (rows near a non-finite value in V take longer and round differently).  n_q may be anything from one
- * token against a long cache to all of them.  (For few queries the keys are split over more
- * CTAs in a small batch than in a large one, so the last bit of a row may depend on the
- * batch; for many it does not.)  B <= 64; heads a multiple of kv_heads, at
+ * token against a long cache to all of them.  (For few queries, up to about 48, the keys are
+ * split over more CTAs in a small batch than in a large one, so the last bit of a row may
+ * depend on the batch; for more queries it does not.)  B <= 64; heads a multiple of kv_heads, at
  * most 1024; q, k, v, out 16-byte aligned; out must not overlap q, k or v.
  * Errors: INVALID_ARG (NULL, misaligned, scale <= 0 or not finite times log2(e), left or
  * right < -1, sinks < 0), SHAPE (B, heads, kv_heads, n_q, n_kv < 1, lengths or starts out of range,
