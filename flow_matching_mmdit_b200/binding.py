@@ -407,6 +407,15 @@ def _whole(where: str, stream, *tensors):
     return out
 
 
+def _rows(where: str, dev: int, x) -> Optional[int]:
+    """Device pointer of a view whose rows are dense (None passes NULL); one of another device is refused."""
+    if x is None:
+        return None
+    if x.get_device() != dev or x.stride(-1) != 1:
+        raise LensError(1, where)
+    return x.data_ptr()
+
+
 def lens_op_quantize_f8(x, x_type: int, rows: int, k: int, block_rows: int, codes, scales, stream=None) -> None:
     px, pc, ps, st = _whole("lens_op_quantize_f8", stream, x, codes, scales)
     _check(load_library().lens_op_quantize_f8(px, x_type, rows, k, block_rows, pc, ps, st),
@@ -423,11 +432,12 @@ def lens_op_sandwich_norm(h, y, y_type: int, M: int, D: int, rows_per_batch: int
                           scale, mod_stride: int, residual_scale: float, eps: float, h_out, out, out_type: int,
                           out_scales=None, stream=None) -> None:
     """gate, shift and scale may be views into one modulation tensor (rows mod_stride apart)."""
-    ph, py, pp, pq, pho, po, pos, st = _whole("lens_op_sandwich_norm", stream, h, y, post_gain, pre_gain, h_out, out,
-                                              out_scales)
-    _check(load_library().lens_op_sandwich_norm(ph, py, y_type, M, D, rows_per_batch, pp, _ptr(gate), pq, _ptr(shift),
-                                                _ptr(scale), mod_stride, residual_scale, eps, pho, po, out_type, pos, st),
-           "lens_op_sandwich_norm")
+    where = "lens_op_sandwich_norm"
+    ph, py, pp, pq, pho, po, pos, st = _whole(where, stream, h, y, post_gain, pre_gain, h_out, out, out_scales)
+    dev = -1 if h is None else h.get_device()
+    _check(load_library().lens_op_sandwich_norm(ph, py, y_type, M, D, rows_per_batch, pp, _rows(where, dev, gate), pq,
+                                                _rows(where, dev, shift), _rows(where, dev, scale), mod_stride,
+                                                residual_scale, eps, pho, po, out_type, pos, st), where)
 
 
 def lens_op_attention_window(q, k, v, B: int, heads: int, kv_heads: int, n_q: int, n_kv: int,

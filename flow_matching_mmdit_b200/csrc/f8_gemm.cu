@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0;
         for (int t = pair; t < a.total_tiles && prod_ok; t += npairs) {
           int tm, tn;
-        tile_of(a, t, tm, tn);
-        const int m0 = tm * 256 + 128 * (int)rank, n0 = tn * BN + (BN / 2) * (int)rank;
+          tile_of(a, t, tm, tn);
+          const int m0 = tm * 256 + 128 * (int)rank, n0 = tn * BN + (BN / 2) * (int)rank;
           for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1, a.err)) {
               prod_ok = false;
@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = true;
       for (int t = pair; t < a.total_tiles && ok; t += npairs) {
         int tm, tn;
-      tile_of(a, t, tm, tn);
-      const int row = tm * 256 + 128 * (int)rank + lane;
+        tile_of(a, t, tm, tn);
+        const int row = tm * 256 + 128 * (int)rank + lane;
         const float* pa = a.as + (int64_t)kb0 * a.M + row;
         // a column block past the last one holds no output: any block's scale will do
         const float* pw = a.ws + (int64_t)kb0 * a.nblocks + min(tn * HALVES + (lane & (HALVES - 1)), a.nblocks - 1);

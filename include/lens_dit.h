@@ -340,9 +340,10 @@ LENS_API lens_status lens_op_attention_masked(const uint16_t* q, const uint16_t*
                                               int n_txt, int n_img, const int* txt_len, uint16_t* out_txt,
                                               uint16_t* out_img, void* stream);
 
-/* The next four operations.  The first call of each on a device loads its kernels, so it
- * belongs in set-up, before a stream capture; later calls can be captured.  They use no
- * workspace: calls on different streams may overlap. */
+/* The next four operations.  A kernel is loaded on a device by the first call that launches it
+ * there, and the sizes and types of a call choose the kernel: make each call once during
+ * set-up, before a stream capture of it.  They use no workspace: calls on different streams
+ * may overlap.  Outputs must not overlap inputs or each other, but for h_out and h. */
 
 /* Element types of the operations below that take more than one. */
 typedef enum lens_dtype {

@@ -145,3 +145,17 @@ def test_sandwich_norm_on_a_side_stream_and_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(h_out, want) and torch.equal(out, want_o)
+
+
+@pytest.mark.parametrize("which", ["gate", "shift", "scale"])
+def test_sandwich_norm_refuses_modulation_that_is_not_on_the_device_or_not_dense(which):
+    M, D = 8, 128
+    t = make(M, D, 8, 9)
+    h_out, out = torch.empty_like(t["h"]), torch.empty((M, D), dtype=torch.bfloat16, device="cuda")
+    for bad in (torch.zeros((1, D)), torch.zeros((1, 2 * D), device="cuda")[:, ::2]):
+        mod = dict(gate=None, shift=None, scale=None)
+        mod[which] = bad
+        with pytest.raises(L.LensError) as ei:
+            L.lens_op_sandwich_norm(t["h"], t["y"], L.LENS_BF16, M, D, 8, None, mod["gate"], None, mod["shift"],
+                                    mod["scale"], D, RS, EPS, h_out, out, L.LENS_BF16)
+        assert ei.value.status == 1

@@ -90,3 +90,15 @@ def test_binding_refuses_host_tensors():
         with pytest.raises(binding.LensError) as ei:
             call()
         assert ei.value.status == BAD
+
+
+def test_binding_refuses_modulation_rows_of_another_device_or_not_dense():
+    import torch
+    x = torch.zeros(4, 6, 128)
+    host = x.get_device()
+    assert binding._rows("norm", host, None) is None
+    assert binding._rows("norm", host, x[:, 2]) == x.data_ptr() + 2 * 128 * 4
+    for dev, bad in ((0, x[:, 0]), (host, x[:, 0].t()), (host, x[:, 0, ::2])):
+        with pytest.raises(binding.LensError) as ei:
+            binding._rows("norm", dev, bad)
+        assert ei.value.status == BAD
