@@ -65,6 +65,11 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ float4 ld_cluster4(const float4* p, uint32_t rank) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -400,6 +405,26 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), int ctas, int cluster, size_t smem, cudaStream_t st,
+                            const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int HALVES, bool BF16, int SPLITS>
 cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
   using C = F8Cfg<HALVES>;
@@ -425,27 +450,280 @@ cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
   a.bias = g.bias;
   a.err = err;
   const int pairs = SPLITS > 1 ? a.total_tiles * SPLITS : (a.total_tiles < sms / 2 ? a.total_tiles : sms / 2);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2 * SPLITS;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, ta, tw, tc, a);
+  return launch_clusters(kernel, 2 * pairs, 2 * SPLITS, C::SMEM, st, ta, tw, tc, a);
 }
 
 template <int HALVES, int SPLITS>
 cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
   return g.bf16 ? launch_pair<HALVES, true, SPLITS>(g, err, sms, st)
                 : launch_pair<HALVES, false, SPLITS>(g, err, sms, st);
+}
+
+// ------------------------------------------------------------------ up to 128 rows
+// Rows of A that fill half a CTA pair's tile at most: bound by reading W once and by the way
+// through the kernel.  One CTA takes 128 rows of W as the M side of the MMAs and all rows of A
+// as their columns, on a share of the k blocks; a cluster of `splits` CTAs shares a tile of W
+// and joins the parts by pushing them into the shared memory of the CTA that finishes a share
+// of the rows of C.  As in the pairs, each k block's product goes to a TMEM slot of its own and
+// is scaled and added in registers: W's scale is one number a tile and block, A's differ by
+// column and are read from shared memory as pairs.
+//   warp 0 TMA;  1, 2 MMA issuers of the even and the odd blocks;  3 scales;
+//   4..11 scale and add: a TMEM lane quarter, half of the columns
+template <int CPW>                                   // columns an adding thread holds
+struct MidCfg {
+  static constexpr int COLS = 2 * CPW, SLOTS = 512 / COLS < 4 ? 512 / COLS : 4;
+  static constexpr uint32_t W_BYTES = 128 * 128, A_BYTES = COLS * 128, STAGE_BYTES = W_BYTES + A_BYTES;
+  static constexpr int STAGES = CPW == 64 ? 4 : 6;
+  static constexpr uint32_t PART_BYTES = COLS * 128 * 4, SCALE_BYTES = SLOTS * COLS * 4, BAR_BYTES = 256;
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + PART_BYTES + SCALE_BYTES + BAR_BYTES;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct MidArgs {
+  F8Gemm g;
+  int kblocks, nblocks, log2_splits;
+  int* err;
+};
+
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+template <int CPW, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1)
+    gemm_f8_mid_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ MidArgs p) {
+  using C = MidCfg<CPW>;
+  constexpr int STAGES = C::STAGES, SLOTS = C::SLOTS, COLS = C::COLS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float4* parts = reinterpret_cast<float4*>(smem + STAGES * C::STAGE_BYTES);   // [CTA][group of 4 rows of C][column]
+  float* sScale = reinterpret_cast<float*>(smem + STAGES * C::STAGE_BYTES + C::PART_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sScale) + C::SCALE_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + SLOTS;
+  uint64_t* sfree = tempty + SLOTS;
+  uint64_t* drain = sfree + SLOTS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  static_assert(STAGES % 2 == 0 && SLOTS % 2 == 0, "two issuers take turns");
+  static_assert((2 * STAGES + 3 * SLOTS + 2) * 8 + 4 <= C::BAR_BYTES, "barriers overflow their reserve");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = 1 << p.log2_splits, rank = blockIdx.x & (splits - 1), tile = blockIdx.x >> p.log2_splits;
+  const int kb0 = p.kblocks * rank >> p.log2_splits, kb1 = p.kblocks * (rank + 1) >> p.log2_splits;
+  auto load = [&](int kb, uint32_t stage) {
+    uint8_t* s = smem + stage * C::STAGE_BYTES;
+    mbar_expect_tx(&full[stage], C::STAGE_BYTES);
+    tma_load_2d(s, &tmW, &full[stage], kb * 128, tile * 128);
+    tma_load_2d(s + C::W_BYTES, &tmA, &full[stage], kb * 128, 0);
+  };
+  cluster_arrive();              // waited for before parts are pushed
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int j = 0; j < SLOTS; ++j) {
+      mbar_init(&tfull[j], 2);
+      mbar_init(&tempty[j], 8);
+      mbar_init(&sfree[j], 8);
+    }
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    fence_mbar_init();
+    // this thread is the producer too: its first loads need nobody else's set-up
+    grid_dependency_wait();
+    for (int i = 0; i < min(STAGES, kb1 - kb0); ++i) load(kb0 + i, i);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_sync();        // set-up above touched only shared memory and TMEM
+
+  uint64_t acc[CPW / 2];
+  const int quarter = warp & 3, half = (warp >> 2) - 1;
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      int issued = min(STAGES, kb1 - kb0);
+      uint32_t stage = 0, phase = 0;
+      for (int i = issued; i < kb1 - kb0; ++i) {
+        ok = mbar_wait(&empty[stage], phase, p.err);
+        if (!ok) break;
+        load(kb0 + i, stage);
+        issued = i + 1;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // after an abort the issuer may not have waited for every stage filled here
+      if (!ok || err_raised(p.err))
+        for (int i = max(issued - STAGES, 0); i < issued; ++i) mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == 2) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = umma_idesc_e4m3(128, COLS);
+      const int odd = warp == 2;
+      bool ok = true;
+      uint32_t stage = odd, phase = 0, slot = odd, use = 0;
+      for (int kb = kb0 + odd; kb < kb1; kb += 2) {
+        ok = mbar_wait(&tempty[slot], use ^ 1, p.err) && mbar_wait(&full[stage], phase, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t wd = umma_desc_sw128(smem_u32(smem + stage * C::STAGE_BYTES));
+        const uint64_t ad = umma_desc_sw128(smem_u32(smem + stage * C::STAGE_BYTES + C::W_BYTES));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) umma_f8(tmem + slot * COLS, wd + 2 * k, ad + 2 * k, idesc, k > 0 ? 1u : 0u);
+        umma_commit(&tfull[slot]);
+        umma_commit(&empty[stage]);
+        if ((stage += 2) >= STAGES) {
+          stage -= STAGES;
+          phase ^= 1;
+        }
+        if ((slot += 2) >= SLOTS) {
+          slot -= SLOTS;
+          use ^= 1;
+        }
+      }
+      if (!ok) umma_drain(&drain[odd]);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // a block's scales, W's and A's multiplied, beside its slot; loaded AHEAD blocks before
+    constexpr int AHEAD = 4, PER = COLS / 32;
+    const float *pa = p.g.a_scales + (int64_t)kb0 * p.g.M + lane, *pw = p.g.w_scales + (int64_t)kb0 * p.nblocks + tile;
+    float sa[AHEAD][PER], sw[AHEAD];
+    auto fetch = [&](float (&a)[PER], float& w, bool in) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) a[i] = in && lane + 32 * i < p.g.M ? __ldg(pa + 32 * i) : 0.f;
+      w = in ? __ldg(pw) : 0.f;
+      pa += p.g.M;
+      pw += p.nblocks;
+    };
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) fetch(sa[d], sw[d], kb0 + d < kb1);
+    uint32_t slot = 0, use = 0;
+    bool ok = true;
+    for (int kb = kb0; ok && kb < kb1; kb += AHEAD) {
+#pragma unroll
+      for (int d = 0; d < AHEAD; ++d) {
+        if (kb + d >= kb1) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sfree[slot], use ^ 1, p.err));
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sScale[slot * COLS + lane + 32 * i] = sa[d][i] * sw[d];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tfull[slot]);
+        fetch(sa[d], sw[d], kb + d + AHEAD < kb1);
+        if (++slot == SLOTS) {
+          slot = 0;
+          use ^= 1;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CPW / 2; ++i) acc[i] = 0ull;
+    const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + half * CPW;
+    uint32_t slot = 0, use = 0;
+    bool ready = false;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!__all_sync(0xffffffffu, ready) && !__all_sync(0xffffffffu, mbar_wait(&tfull[slot], use, p.err))) break;
+      tc_fence_after();
+      float r[CPW / 32][32];
+#pragma unroll
+      for (int i = 0; i < CPW / 32; ++i) tmem_ld32(at + slot * COLS + 32 * i, r[i]);
+      const float* s = sScale + slot * COLS + half * CPW;
+      const uint32_t was = slot;
+      tmem_ld_wait(r[0]);
+#pragma unroll
+      for (int i = 1; i < CPW / 32; ++i) tmem_ld_pin(r[i]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[was]);
+      if (++slot == SLOTS) {
+        slot = 0;
+        use ^= 1;
+      }
+      ready = mbar_test(&tfull[slot], use);      // asked ahead of the adds that hide it
+#pragma unroll
+      for (int i = 0; i < CPW / 4; ++i) {
+        const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(s + 4 * i);
+        acc[2 * i] = f2_fma(f2_pack(r[i / 8][4 * (i % 8)], r[i / 8][4 * (i % 8) + 1]), s4.x, acc[2 * i]);
+        acc[2 * i + 1] = f2_fma(f2_pack(r[i / 8][4 * (i % 8) + 2], r[i / 8][4 * (i % 8) + 3]), s4.y, acc[2 * i + 1]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfree[was]);
+    }
+  }
+  // ---- join: group q of four rows of C goes to CTA q % splits
+  cluster_wait();
+  const int per = COLS / 4 >> p.log2_splits, n = quarter * 32 + lane;
+  if (warp >= 4) {
+#pragma unroll
+    for (int i = 0; i < CPW / 4; ++i) {
+      const int q = half * (CPW / 4) + i;
+      if (4 * q >= p.g.M) break;
+      float4 v;
+      f2_unpack(acc[2 * i], v.x, v.y);
+      f2_unpack(acc[2 * i + 1], v.z, v.w);
+      st_cluster4(mapa_shared(smem_u32(parts + (rank * per + (q >> p.log2_splits)) * 128 + n), q & (splits - 1)), v);
+    }
+  }
+  tc_fence_before();
+  cluster_arrive();
+  cluster_wait();
+  if (warp >= 4 && !err_raised(p.err)) {
+    const int col = tile * 128 + n;
+    const float bias = p.g.bias && col < p.g.N ? __ldg(p.g.bias + col) : 0.f;
+#pragma unroll 4
+    for (int l = half; l < per; l += 2) {
+      const int m = 4 * ((l << p.log2_splits) + rank);
+      if (m >= p.g.M || col >= p.g.N) break;
+      float4 y = parts[l * 128 + n];
+      for (int k = 1; k < splits; ++k) {
+        const float4 v = parts[(k * per + l) * 128 + n];
+        y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+      }
+      const float o[4] = {y.x + bias, y.y + bias, y.z + bias, y.w + bias};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (m + i < p.g.M) {
+          const int64_t to = (int64_t)(m + i) * p.g.N + col;
+          if (BF16)
+            static_cast<__nv_bfloat16*>(p.g.C)[to] = __float2bfloat16_rn(o[i]);
+          else
+            static_cast<float*>(p.g.C)[to] = o[i];
+        }
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int CPW, bool BF16>
+cudaError_t launch_mid(const F8Gemm& g, int log2_splits, int* err, cudaStream_t st) {
+  using C = MidCfg<CPW>;
+  CUtensorMap ta, tw;
+  if (!encode_tmap_u8(&ta, g.A, g.M, g.K, C::COLS) || !encode_tmap_u8(&tw, g.W, g.N, g.K, 128))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> attr{0};
+  const auto kernel = gemm_f8_mid_kernel<CPW, BF16>;
+  const cudaError_t e = ensure_smem_limit(kernel, (int)C::SMEM, attr);
+  if (e != cudaSuccess) return e;
+  const MidArgs p{g, (g.K + kF8Group - 1) / kF8Group, (g.N + kF8Group - 1) / kF8Group, log2_splits, err};
+  return launch_clusters(kernel, p.nblocks << log2_splits, 1 << log2_splits, C::SMEM, st, ta, tw, p);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -538,12 +816,27 @@ cudaError_t launch_few(const F8Gemm& g, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_gemm_f8(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
-  // 4608 x 1536, us: 1 row 3.4 (CTA pairs 9.3), 8 rows 3.9 (8.5), 16 rows 5.1 (8.1), 32 rows
-  // 7.7 (8.0); 1536 x 4096: 16 rows 4.3 (12.6), 32 rows 7.0 (12.7)
-  if (g.M <= 8) return launch_few<1>(g, st);
-  if (g.M <= 16) return launch_few<2>(g, st);
-  if (g.M <= 32) return launch_few<4>(g, st);
-  const int64_t tiles_m = (g.M + 255) / 256, pairs = sms / 2, kblocks = (g.K + kF8Group - 1) / kF8Group;
+  const int64_t kblocks = (g.K + kF8Group - 1) / kF8Group, weights = (int64_t)g.N * g.K;
+  // Up to 32 rows, few weights and no long k.  us, mma.sync for 128-row tiles of W by tcgen05:
+  // 8 rows, 4608 x 1536 3.4 for 4.6, 4096 x 8192 11.0 for 8.7; 16 rows, 1536 x 4096 4.0 for 4.4,
+  // 8192 x 1536 7.5 for 5.3, 128 x 11520 6.9 for 5.6; 32 rows, 2304 x 1536 3.9 for 4.1,
+  // 1536 x 4096 6.5 for 4.6.
+  const int groups = g.M <= 8 ? 1 : g.M <= 16 ? 2 : 4;
+  if (g.M <= 32 && groups * weights <= 1 << 24 && groups * kblocks <= 96)
+    return groups == 1 ? launch_few<1>(g, st) : groups == 2 ? launch_few<2>(g, st) : launch_few<4>(g, st);
+  // Up to 128 rows: as many CTAs a tile of W as there are k blocks for, while all clusters find
+  // room at once (of 36 clusters of four CTAs one waits: 4608 x 1536, 64 rows 8.9 us for 5.6
+  // with two).  us, 128-row tiles of W for CTA pairs: 64 rows, 1536 x 4096 5.2 for 8.4, 4096 x
+  // 8192 9.9 for 21.5, 24576 x 1536 16.7 for 17.4; 77 rows, 1536 x 4096 6.1 for 8.4, 16384 x
+  // 2048 12.5 for 14.7, 24576 x 1536 19.8 for 17.6 (more tiles than SMs).
+  const int64_t tiles = (g.N + kF8Group - 1) / kF8Group;
+  if (g.M <= 64 || (g.M <= 128 && tiles <= sms)) {
+    int l2 = 0;
+    while (l2 < 3 && kblocks >= 2 << l2 && 8 * (2 * tiles << l2) <= 7 * sms) ++l2;
+    if (g.M <= 64) return g.bf16 ? launch_mid<32, true>(g, l2, err, st) : launch_mid<32, false>(g, l2, err, st);
+    return g.bf16 ? launch_mid<64, true>(g, l2, err, st) : launch_mid<64, false>(g, l2, err, st);
+  }
+  const int64_t tiles_m = (g.M + 255) / 256, pairs = sms / 2;
   const int64_t narrow_tiles = tiles_m * ((g.N + 127) / 128), wide_tiles = tiles_m * ((g.N + 255) / 256);
   // Few tiles and a long k: four pairs a tile, while their clusters of eight CTAs find room
   // beside each other.  77 x 1536 x 4096 (32 k blocks): 8.4 us for 13.0; 256 x 1536 x 1536 (12):
