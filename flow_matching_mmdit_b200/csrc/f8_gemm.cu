@@ -38,8 +38,6 @@ namespace {
 // alone would take 150 and L2 delivers a pair's 48 KB in 230 (10 TB/s, as for the bf16
 // products); the rest is the way through a slot (MMA, commit, read, release, next MMA), of
 // which four run at a time, or two of twice the width.
-// SPLIT: a cluster of several pairs works on one tile, each on its part of the k blocks, and
-// joins the parts through distributed shared memory.
 template <int HALVES>
 struct F8Cfg {
   static constexpr int BN = 128 * HALVES, COLS = BN / 2;   // COLS: columns a thread accumulates
@@ -65,22 +63,7 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float4 ld_cluster4(const float4* p, uint32_t rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(mapa_shared(smem_u32(p), rank))
-               : "memory");
-  return v;
-}
-
 struct F8GemmArgs {
-  void* C;
   int M, N, kblocks, tiles_m, tiles_n, total_tiles, nblocks;
   const float *as, *ws, *bias;
   int* err;
@@ -97,12 +80,11 @@ __device__ __forceinline__ void tile_of(const F8GemmArgs& a, int t, int& tm, int
   tm = first + l - tn * rows;
 }
 
-template <int HALVES, bool BF16, int SPLITS>
+template <int HALVES, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmC, const F8GemmArgs a) {
   using C = F8Cfg<HALVES>;
-  constexpr bool SPLIT = SPLITS > 1;
   constexpr int STAGES = C::STAGES, SLOTS = C::SLOTS, BN = C::BN, COLS = C::COLS, SCALES = C::SCALES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -121,13 +103,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   static_assert((2 * STAGES + 3 * SLOTS + 2) * 8 + 8 <= C::BAR_BYTES, "barriers overflow their reserve");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // this CTA's rank in its pair, and the pair's leader in the cluster
-  const uint32_t rank = SPLIT ? cluster_ctarank() & 1 : cluster_ctarank(), base = SPLIT ? cluster_ctarank() & ~1u : 0;
-  const uint16_t both = 0x3 << base;
-  // SPLIT: one tile a cluster, the k blocks [kb0, kb1) of it a pair
-  const int pair = SPLIT ? blockIdx.x / (2 * SPLITS) : blockIdx.x >> 1, npairs = SPLIT ? a.total_tiles : gridDim.x >> 1;
-  const int kb0 = SPLIT ? a.kblocks * (int)(base >> 1) / SPLITS : 0;
-  const int kb1 = SPLIT ? a.kblocks * (int)((base >> 1) + 1) / SPLITS : a.kblocks;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -171,7 +148,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           int tm, tn;
           tile_of(a, t, tm, tn);
           const int m0 = tm * 256 + 128 * (int)rank, n0 = tn * BN + (BN / 2) * (int)rank;
-          for (int kb = kb0; kb < kb1; ++kb) {
+          for (int kb = 0; kb < a.kblocks; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1, a.err)) {
               prod_ok = false;
               break;
@@ -189,7 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         // the leader reconciles both CTAs' loads if the pair aborts
-        if (rank == 1) st_shared_cluster_u32(mapa_shared(smem_u32(peer_issued), base), prod_issued);
+        if (rank == 1) st_shared_cluster_u32(mapa_shared(smem_u32(peer_issued), 0), prod_issued);
       }
       __syncwarp();
     } else if (warp == 1 || warp == 2) {
@@ -198,7 +175,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t odd = warp == 2;
         bool ok = true;
         uint32_t stage = odd, phase = 0, slot = odd, use = 0;
-        const int64_t blocks = (int64_t)((a.total_tiles - pair + npairs - 1) / npairs) * (kb1 - kb0);
+        const int64_t blocks = (int64_t)((a.total_tiles - pair + npairs - 1) / npairs) * a.kblocks;
         for (int64_t i = odd; i < blocks; i += 2) {
           if (!mbar_wait_sleep(&tempty[slot], use ^ 1, a.err) || !mbar_wait_sleep(&full[stage], phase, a.err)) {
             ok = false;
@@ -209,8 +186,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint64_t wd = umma_desc_sw128(smem_u32(sW + stage * C::B_BYTES));
 #pragma unroll
           for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + slot * BN, ad + 2 * k, wd + 2 * k, idesc, k > 0 ? 1u : 0u);
-          umma_commit_pair(&empty[stage], both);
-          umma_commit_pair(&tfull[slot], both);
+          umma_commit_pair(&empty[stage], 0x3);
+          umma_commit_pair(&tfull[slot], 0x3);
           if ((stage += 2) >= STAGES) {
             stage -= STAGES;
             phase ^= 1;
@@ -220,7 +197,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             use ^= 1;
           }
         }
-        if (!ok) umma_drain_pair(&drain[odd], (uint16_t)(1u << base));
+        if (!ok) umma_drain_pair(&drain[odd]);
       }
       __syncwarp();
     } else {
@@ -230,10 +207,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         int tm, tn;
         tile_of(a, t, tm, tn);
         const int row = tm * 256 + 128 * (int)rank + lane;
-        const float* pa = a.as + (int64_t)kb0 * a.M + row;
+        const float* pa = a.as + row;
         // a column block past the last one holds no output: any block's scale will do
-        const float* pw = a.ws + (int64_t)kb0 * a.nblocks + min(tn * HALVES + (lane & (HALVES - 1)), a.nblocks - 1);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        const float* pw = a.ws + min(tn * HALVES + (lane & (HALVES - 1)), a.nblocks - 1);
+        for (int kb = 0; kb < a.kblocks; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&sfree[slot], use ^ 1, a.err))) {
             ok = false;
             break;
@@ -262,7 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3, part = (warp - 4) >> 2;
     uint8_t* box = sEpi + (warp - 4) * 4096;
     const uint32_t lane_addr = tmem + (uint32_t(quarter * 32) << 16) + part * COLS;
-    const uint32_t leader_tempty = mapa_shared(smem_u32(&tempty[0]), base);
+    const uint32_t leader_tempty = mapa_shared(smem_u32(&tempty[0]), 0);
     const float* a_scale = sScale + quarter * 32 + lane;
     const float* w_scale = sScale + 128 + (HALVES == 1 ? 0 : part);
     uint32_t slot = 0, use = 0, no_box = 0;
@@ -272,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
 #pragma unroll 1
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = 0; kb < a.kblocks; ++kb) {
         if (!__all_sync(0xffffffffu, ready) && !__all_sync(0xffffffffu, mbar_wait(&tfull[slot], use, a.err))) {
           ok = false;
           break;
@@ -317,19 +294,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       tile_of(a, t, tm, tn);
       const int row0 = tm * 256 + 128 * (int)rank + quarter * 32;
       const int n0 = tn * BN + part * COLS;
-      if constexpr (SPLIT) {
-        // this pair's part of the sum, [part][16-byte piece of the columns][row]; the stages
-        // are free: every MMA has completed
-        float4* mine = reinterpret_cast<float4*>(smem) + part * 16 * 128 + quarter * 32 + lane;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float4 v;
-          f2_unpack(acc[2 * c], v.x, v.y);
-          f2_unpack(acc[2 * c + 1], v.z, v.w);
-          mine[128 * c] = v;
-        }
-        continue;
-      }
       constexpr int PER = BF16 ? 64 : 32;        // columns of one 128-byte box row
 #pragma unroll
       for (int c = 0; c < COLS / PER; ++c) {
@@ -360,45 +324,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 
   tc_fence_before();
-  cluster_sync_all();          // every role of the cluster's CTAs has left its loop
-  if constexpr (SPLIT) {
-    // each of the cluster's pairs finishes a share of the columns, adding the pairs' parts in order
-    if (warp >= 4 && !err_raised(a.err)) {
-      const int quarter = warp & 3, part = (warp - 4) >> 2;
-      int tm, tn;
-      tile_of(a, pair, tm, tn);
-      const int row = tm * 256 + 128 * (int)rank + quarter * 32 + lane;
-      constexpr int SHARE = 16 / SPLITS;
-      const int first = SHARE * (int)(base >> 1);
-      const float4* mine = reinterpret_cast<const float4*>(smem) + part * 16 * 128 + quarter * 32 + lane;
-      float4 v[SHARE][SPLITS];
-#pragma unroll
-      for (int c = 0; c < SHARE; ++c)
-#pragma unroll
-        for (int p = 0; p < SPLITS; ++p) v[c][p] = ld_cluster4(mine + 128 * (first + c), 2 * p + rank);
-#pragma unroll
-      for (int c = 0; c < SHARE; ++c) {
-        const int n = tn * BN + part * COLS + 4 * (first + c);
-        if (row >= a.M || n >= a.N) continue;
-        float4 y = v[c][0];
-#pragma unroll
-        for (int p = 1; p < SPLITS; ++p) y.x += v[c][p].x, y.y += v[c][p].y, y.z += v[c][p].z, y.w += v[c][p].w;
-        if (a.bias) {
-          y.x += __ldg(a.bias + n), y.y += __ldg(a.bias + n + 1);
-          y.z += __ldg(a.bias + n + 2), y.w += __ldg(a.bias + n + 3);
-        }
-        const int64_t at = (int64_t)row * a.N + n;
-        if (BF16)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.C) + at) =
-              make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-        else
-          *reinterpret_cast<float4*>(static_cast<float*>(a.C) + at) = y;
-      }
-    }
-  }
+  cluster_sync_all();          // every role of both CTAs has left its loop; rank 1's count is in place
   if (warp == 0 && lane == 0 && rank == 0 && (!prod_ok || err_raised(a.err)))
     drain_pair_stages<STAGES>(full, [&](uint32_t) { return C::STAGE_BYTES; }, prod_issued, *peer_issued);
-  cluster_sync_all();          // no MMA, TMA, remote arrive or remote read of the cluster is in flight
+  cluster_sync_all();          // no MMA, TMA or remote arrive of the pair is still in flight
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
@@ -406,10 +335,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(KArgs...), int ctas, int cluster, size_t smem, cudaStream_t st,
+cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 ctas, int cluster, size_t smem, cudaStream_t st,
                             const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = ctas;
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -425,7 +354,7 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), int ctas, int cluster, siz
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int HALVES, bool BF16, int SPLITS>
+template <int HALVES, bool BF16>
 cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
   using C = F8Cfg<HALVES>;
   CUtensorMap ta, tw, tc;
@@ -433,11 +362,10 @@ cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
       !encode_tmap_out(&tc, g.C, BF16 ? 2 : 4, g.M, g.N, g.N))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> attr{0};
-  const auto kernel = gemm_f8_pair_kernel<HALVES, BF16, SPLITS>;
+  const auto kernel = gemm_f8_pair_kernel<HALVES, BF16>;
   const cudaError_t e = ensure_smem_limit(kernel, (int)C::SMEM, attr);
   if (e != cudaSuccess) return e;
   F8GemmArgs a;
-  a.C = g.C;
   a.M = g.M;
   a.N = g.N;
   a.kblocks = (g.K + kF8Group - 1) / kF8Group;
@@ -449,24 +377,25 @@ cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
   a.ws = g.w_scales;
   a.bias = g.bias;
   a.err = err;
-  const int pairs = SPLITS > 1 ? a.total_tiles * SPLITS : (a.total_tiles < sms / 2 ? a.total_tiles : sms / 2);
-  return launch_clusters(kernel, 2 * pairs, 2 * SPLITS, C::SMEM, st, ta, tw, tc, a);
+  const int pairs = a.total_tiles < sms / 2 ? a.total_tiles : sms / 2;
+  return launch_clusters(kernel, dim3(2 * pairs), 2, C::SMEM, st, ta, tw, tc, a);
 }
 
-template <int HALVES, int SPLITS>
+template <int HALVES>
 cudaError_t launch_pair(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
-  return g.bf16 ? launch_pair<HALVES, true, SPLITS>(g, err, sms, st)
-                : launch_pair<HALVES, false, SPLITS>(g, err, sms, st);
+  return g.bf16 ? launch_pair<HALVES, true>(g, err, sms, st) : launch_pair<HALVES, false>(g, err, sms, st);
 }
 
-// ------------------------------------------------------------------ up to 128 rows
-// Rows of A that fill half a CTA pair's tile at most: bound by reading W once and by the way
-// through the kernel.  One CTA takes 128 rows of W as the M side of the MMAs and all rows of A
-// as their columns, on a share of the k blocks; a cluster of `splits` CTAs shares a tile of W
+// ------------------------------------------------------------------ few tiles
+// Up to 128 rows of A, or too few tiles for the pairs: bound by reading W once and by the way
+// through the kernel.  One CTA takes 128 rows of W as the M side of the MMAs and up to 128 rows
+// of A as their columns, on a share of the k blocks; a cluster of `splits` CTAs shares a tile
 // and joins the parts by pushing them into the shared memory of the CTA that finishes a share
-// of the rows of C.  As in the pairs, each k block's product goes to a TMEM slot of its own and
-// is scaled and added in registers: W's scale is one number a tile and block, A's differ by
-// column and are read from shared memory as pairs.
+// of the rows of C (one cluster barrier; parts pulled by the finishing CTAs took about 3 us).
+// As in the pairs, each k block's product goes to a TMEM slot of its own and is scaled and added
+// in registers: W's scale is one number a tile and block, A's differ by column, and their
+// products are read from shared memory as pairs.  A k block takes 210 ns with 64 columns, 320
+// with 128.
 //   warp 0 TMA;  1, 2 MMA issuers of the even and the odd blocks;  3 scales;
 //   4..11 scale and add: a TMEM lane quarter, half of the columns
 template <int CPW>                                   // columns an adding thread holds
@@ -512,12 +441,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = 1 << p.log2_splits, rank = blockIdx.x & (splits - 1), tile = blockIdx.x >> p.log2_splits;
+  const int first = blockIdx.y * COLS, rows = p.g.M - first;      // of A
   const int kb0 = p.kblocks * rank >> p.log2_splits, kb1 = p.kblocks * (rank + 1) >> p.log2_splits;
   auto load = [&](int kb, uint32_t stage) {
     uint8_t* s = smem + stage * C::STAGE_BYTES;
     mbar_expect_tx(&full[stage], C::STAGE_BYTES);
     tma_load_2d(s, &tmW, &full[stage], kb * 128, tile * 128);
-    tma_load_2d(s + C::W_BYTES, &tmA, &full[stage], kb * 128, 0);
+    tma_load_2d(s + C::W_BYTES, &tmA, &full[stage], kb * 128, first);
   };
   cluster_arrive();              // waited for before parts are pushed
   if (threadIdx.x == 0) {
@@ -600,11 +530,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 3) {
     // a block's scales, W's and A's multiplied, beside its slot; loaded AHEAD blocks before
     constexpr int AHEAD = 4, PER = COLS / 32;
-    const float *pa = p.g.a_scales + (int64_t)kb0 * p.g.M + lane, *pw = p.g.w_scales + (int64_t)kb0 * p.nblocks + tile;
+    const float* pa = p.g.a_scales + (int64_t)kb0 * p.g.M + first + lane;
+    const float* pw = p.g.w_scales + (int64_t)kb0 * p.nblocks + tile;
     float sa[AHEAD][PER], sw[AHEAD];
     auto fetch = [&](float (&a)[PER], float& w, bool in) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) a[i] = in && lane + 32 * i < p.g.M ? __ldg(pa + 32 * i) : 0.f;
+      for (int i = 0; i < PER; ++i) a[i] = in && lane + 32 * i < rows ? __ldg(pa + 32 * i) : 0.f;
       w = in ? __ldg(pw) : 0.f;
       pa += p.g.M;
       pw += p.nblocks;
@@ -672,7 +603,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
     for (int i = 0; i < CPW / 4; ++i) {
       const int q = half * (CPW / 4) + i;
-      if (4 * q >= p.g.M) break;
+      if (4 * q >= rows) break;
       float4 v;
       f2_unpack(acc[2 * i], v.x, v.y);
       f2_unpack(acc[2 * i + 1], v.z, v.w);
@@ -688,7 +619,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 4
     for (int l = half; l < per; l += 2) {
       const int m = 4 * ((l << p.log2_splits) + rank);
-      if (m >= p.g.M || col >= p.g.N) break;
+      if (m >= rows || col >= p.g.N) break;
       float4 y = parts[l * 128 + n];
       for (int k = 1; k < splits; ++k) {
         const float4 v = parts[(k * per + l) * 128 + n];
@@ -697,8 +628,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float o[4] = {y.x + bias, y.y + bias, y.z + bias, y.w + bias};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (m + i < p.g.M) {
-          const int64_t to = (int64_t)(m + i) * p.g.N + col;
+        if (m + i < rows) {
+          const int64_t to = (int64_t)(first + m + i) * p.g.N + col;
           if (BF16)
             static_cast<__nv_bfloat16*>(p.g.C)[to] = __float2bfloat16_rn(o[i]);
           else
@@ -723,7 +654,8 @@ cudaError_t launch_mid(const F8Gemm& g, int log2_splits, int* err, cudaStream_t 
   const cudaError_t e = ensure_smem_limit(kernel, (int)C::SMEM, attr);
   if (e != cudaSuccess) return e;
   const MidArgs p{g, (g.K + kF8Group - 1) / kF8Group, (g.N + kF8Group - 1) / kF8Group, log2_splits, err};
-  return launch_clusters(kernel, p.nblocks << log2_splits, 1 << log2_splits, C::SMEM, st, ta, tw, p);
+  return launch_clusters(kernel, dim3(p.nblocks << log2_splits, (g.M + C::COLS - 1) / C::COLS), 1 << log2_splits,
+                         C::SMEM, st, ta, tw, p);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -824,31 +756,28 @@ cudaError_t launch_gemm_f8(const F8Gemm& g, int* err, int sms, cudaStream_t st) 
   const int groups = g.M <= 8 ? 1 : g.M <= 16 ? 2 : 4;
   if (g.M <= 32 && groups * weights <= 1 << 24 && groups * kblocks <= 96)
     return groups == 1 ? launch_few<1>(g, st) : groups == 2 ? launch_few<2>(g, st) : launch_few<4>(g, st);
-  // Up to 128 rows: as many CTAs a tile of W as there are k blocks for, while all clusters find
-  // room at once (of 36 clusters of four CTAs one waits: 4608 x 1536, 64 rows 8.9 us for 5.6
-  // with two).  us, 128-row tiles of W for CTA pairs: 64 rows, 1536 x 4096 5.2 for 8.4, 4096 x
-  // 8192 9.9 for 21.5, 24576 x 1536 16.7 for 17.4; 77 rows, 1536 x 4096 6.1 for 8.4, 16384 x
-  // 2048 12.5 for 14.7, 24576 x 1536 19.8 for 17.6 (more tiles than SMs).
-  const int64_t tiles = (g.N + kF8Group - 1) / kF8Group;
-  if (g.M <= 64 || (g.M <= 128 && tiles <= sms)) {
-    int l2 = 0;
-    while (l2 < 3 && kblocks >= 2 << l2 && 8 * (2 * tiles << l2) <= 7 * sms) ++l2;
-    if (g.M <= 64) return g.bf16 ? launch_mid<32, true>(g, l2, err, st) : launch_mid<32, false>(g, l2, err, st);
+  // 128 x 128 tiles, each with as many CTAs as there are k blocks for while all clusters find
+  // room at once (of 36 clusters of four CTAs one waits: 4608 x 1536, 64 rows 8.9 us for 5.6 with
+  // two): where there is one row of tiles or room for two CTAs a tile.  us, for CTA pairs: 64
+  // rows, 1536 x 4096 5.3 for 8.4, 4096 x 8192 9.9 for 21.5, 24576 x 1536 16.7 for 18.4; 77 rows,
+  // 1536 x 4096 6.1 for 8.5, 16384 x 2048 12.6 for 14.7, 24576 x 1536 (more tiles than SMs) 19.8
+  // for 17.4; 200 rows, 1536 x 1536 6.4 for 7.6, 1536 x 4096 8.4 for 12.9, 4608 x 1536 (no room
+  // for two) 9.4 for 8.0; 640 rows, 768 x 4096 8.7 for 13.1, 1536 x 1536 8.0 for 8.0.
+  const int64_t tiles = (g.N + kF8Group - 1) / kF8Group * (g.M <= 64 ? 1 : (g.M + 127) / 128);
+  int l2 = 0;
+  while (l2 < 3 && kblocks >= 2 << l2 && 8 * (2 * tiles << l2) <= 7 * sms) ++l2;
+  if (g.M <= 64) return g.bf16 ? launch_mid<32, true>(g, l2, err, st) : launch_mid<32, false>(g, l2, err, st);
+  if (l2 > 0 || (g.M <= 128 && tiles <= sms))
     return g.bf16 ? launch_mid<64, true>(g, l2, err, st) : launch_mid<64, false>(g, l2, err, st);
-  }
   const int64_t tiles_m = (g.M + 255) / 256, pairs = sms / 2;
   const int64_t narrow_tiles = tiles_m * ((g.N + 127) / 128), wide_tiles = tiles_m * ((g.N + 255) / 256);
-  // Few tiles and a long k: four pairs a tile, while their clusters of eight CTAs find room
-  // beside each other.  77 x 1536 x 4096 (32 k blocks): 8.4 us for 13.0; 256 x 1536 x 1536 (12):
-  // 7.9 for 7.5, the join costs as much as nine blocks.
-  if (20 * narrow_tiles <= 4 * pairs && kblocks >= 20) return launch_pair<1, 4>(g, err, sms, st);
   // 256-wide tiles load and wait less a column, but only where their rounds on the pairs
   // come near half of the 128-wide ones': sustained, us, 8704 x 8192 x 1536 (15 rounds for 30)
   // 135 for 142, 8704 x 1536 x 4096 (3 for 6) 65 for 72, 4352 x 4608 x 1536 (5 for 9) 43 for
   // 44, 4352 x 1536 x 4096 (2 for 3) 39 for 37, 1152 x 8192 x 1536 (3 for 5) 26 for 23
   const int64_t wide = (wide_tiles + pairs - 1) / pairs, narrow = (narrow_tiles + pairs - 1) / pairs;
-  if (7 * wide <= 4 * narrow) return launch_pair<2, 1>(g, err, sms, st);
-  return launch_pair<1, 1>(g, err, sms, st);
+  if (7 * wide <= 4 * narrow) return launch_pair<2>(g, err, sms, st);
+  return launch_pair<1>(g, err, sms, st);
 }
 
 }  // namespace lens

@@ -210,6 +210,11 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Its two halves.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Shared-memory address of the same variable in CTA `rank` of this cluster.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -348,8 +353,8 @@ __device__ __forceinline__ void umma_drain(uint64_t* bar) {
 }
 // The same for the leader of a CTA pair (the pair's UMMAs write both CTAs' TMEM);
 // the commit arrives on the leader's `bar` only.
-__device__ __forceinline__ void umma_drain_pair(uint64_t* bar, uint16_t leader = 0x1) {
-  umma_commit_pair(bar, leader);
+__device__ __forceinline__ void umma_drain_pair(uint64_t* bar) {
+  umma_commit_pair(bar, 0x1);
   mbar_wait_drain(bar, 0);
 }
 

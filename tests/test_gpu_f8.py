@@ -119,7 +119,9 @@ def check_gemm(c, codes_a, sa, codes_w, sw, bias, K, bf16):
 SIZES = [(1, 16, 16), (1, 4608, 1536), (2, 144, 400), (8, 1536, 4096), (9, 272, 1552), (16, 8192, 1536), (17, 128, 128),
          (33, 2000, 2880), (77, 1536, 4096), (128, 256, 384), (129, 400, 144), (255, 512, 1536), (333, 4608, 1536),
          (513, 1040, 2896), (1152, 1536, 1536), (4352, 1536, 4096),
-         (40, 16, 16), (300, 16, 272), (64, 1536, 2576), (200, 400, 11520), (1500, 8192, 400), (2100, 4624, 144)]
+         (40, 16, 16), (300, 16, 272), (64, 1536, 2576), (200, 400, 11520), (1500, 8192, 400), (2100, 4624, 144),
+         (24, 8192, 1536), (50, 24576, 144), (64, 4096, 8192), (65, 144, 11520), (100, 19200, 144), (129, 2320, 1040),
+         (300, 768, 4096), (640, 1536, 1536)]
 
 
 @pytest.mark.parametrize("bf16", [False, True])
