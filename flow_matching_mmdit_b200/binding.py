@@ -394,7 +394,8 @@ def _whole(where: str, stream, *tensors):
             continue
         at = x.get_device()
         if at != dev:
-            if at < 0 or dev is not None or at != torch.cuda.current_device():
+            # (the raw call: there is a device tensor, so CUDA is up)
+            if at < 0 or dev is not None or at != torch._C._cuda_getDevice():
                 raise LensError(1, where)
             dev = at
         if not x.is_contiguous():
