@@ -92,3 +92,40 @@ def test_attention_half_of_a_block():
     assert rel(out, xs @ W.t() + bias.double()) < 0.04
     assert rel(out, xr @ W.t() + bias.double()) < 0.2
     assert np.isfinite(float(out.sum()))
+
+
+def test_operations_on_several_streams_at_once():
+    """Products of each kernel and both attention kernels, shuffled over four streams: the same bits as alone."""
+    rng = np.random.default_rng(3)
+    jobs = []
+    for M, N, K in ((8, 768, 1536), (77, 768, 2576), (300, 400, 1536), (1100, 2320, 272)):
+        x = torch.from_numpy(rng.standard_normal((M + N, K)).astype(np.float32)).cuda()
+        groups = -(-K // 128)
+        ca, sa = torch.empty((M, K), dtype=torch.uint8, device="cuda"), torch.empty((groups, M), device="cuda")
+        cw, sw = torch.empty((N, K), dtype=torch.uint8, device="cuda"), torch.empty((groups, -(-N // 128)), device="cuda")
+        L.lens_op_quantize_f8(x[:M], L.LENS_F32, M, K, 1, ca, sa)
+        L.lens_op_quantize_f8(x[M:], L.LENS_F32, N, K, 128, cw, sw)
+        c = torch.empty((M, N), device="cuda")
+        jobs.append((lambda st, a=(ca, sa, cw, sw, None, c, L.LENS_F32, M, N, K): L.lens_op_gemm_f8(*a, stream=st), c))
+    for n_q, n_kv in ((1, 1500), (40, 700), (300, 1500)):
+        q = torch.from_numpy(rng.standard_normal((2, 6, n_q, 64)).astype(np.float32)).cuda().to(torch.bfloat16)
+        k, v = (torch.from_numpy(rng.standard_normal((2, 3, n_kv, 64)).astype(np.float32)).cuda().to(torch.bfloat16)
+                for _ in range(2))
+        o = torch.empty((2, n_q, 384), dtype=torch.bfloat16, device="cuda")
+        a = (q, k, v, 2, 6, 3, n_q, n_kv, [n_kv - n_q] * 2, None, 400, 0, 4, 0.125, o)
+        jobs.append((lambda st, a=a: L.lens_op_attention_window(*a, stream=st), o))
+    want = []
+    for call, out in jobs:
+        call(None)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(10):
+        for _, out in jobs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for i, job in enumerate(rng.permutation(len(jobs))):
+            jobs[job][0](streams[i % 4])
+        torch.cuda.synchronize()
+        for (_, out), w in zip(jobs, want):
+            assert torch.equal(out, w)
