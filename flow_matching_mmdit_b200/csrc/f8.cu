@@ -136,3 +136,14 @@ extern "C" lens_status lens_op_gemm_f8(const uint8_t* A, const float* a_scales, 
   const F8Gemm g{A, W, a_scales, w_scales, bias, C, c_type == LENS_BF16, M, N, K};
   return launch_gemm_f8(g, err, device_sms(), (cudaStream_t)stream) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
 }
+
+extern "C" lens_status lens_op_quantize_f8_block(const lens_quantize_f8_args* a) {
+  if (!a) return LENS_ERR_INVALID_ARG;
+  return lens_op_quantize_f8(a->x, (lens_dtype)a->x_type, a->rows, a->k, a->block_rows, a->codes, a->scales, a->stream);
+}
+
+extern "C" lens_status lens_op_gemm_f8_block(const lens_gemm_f8_args* a) {
+  if (!a) return LENS_ERR_INVALID_ARG;
+  return lens_op_gemm_f8(a->A, a->a_scales, a->W, a->w_scales, a->bias, a->C, (lens_dtype)a->c_type, a->M, a->N, a->K,
+                         a->stream);
+}

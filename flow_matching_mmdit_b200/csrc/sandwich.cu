@@ -214,3 +214,10 @@ extern "C" lens_status lens_op_sandwich_norm(const float* h, const void* y, lens
                                   : launch_sandwich<false, false>(a, sms, st));
   return e == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
 }
+
+extern "C" lens_status lens_op_sandwich_norm_block(const lens_sandwich_norm_args* a) {
+  if (!a) return LENS_ERR_INVALID_ARG;
+  return lens_op_sandwich_norm(a->h, a->y, (lens_dtype)a->y_type, a->M, a->D, a->rows_per_batch, a->post_gain, a->gate,
+                               a->pre_gain, a->shift, a->scale, a->mod_stride, a->residual_scale, a->eps, a->h_out,
+                               a->out, (lens_dtype)a->out_type, a->out_scales, a->stream);
+}

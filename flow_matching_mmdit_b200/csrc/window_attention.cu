@@ -896,3 +896,9 @@ extern "C" lens_status lens_op_attention_window(const uint16_t* q, const uint16_
   if (!err) return LENS_ERR_CUDA;
   return launch_many(a, spans, B, err, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
 }
+
+extern "C" lens_status lens_op_attention_window_block(const lens_attention_window_args* a) {
+  if (!a) return LENS_ERR_INVALID_ARG;
+  return lens_op_attention_window(a->q, a->k, a->v, a->B, a->heads, a->kv_heads, a->n_q, a->n_kv, a->q_start, a->kv_len,
+                                  a->left, a->right, a->sinks, a->scale, a->out, a->stream);
+}

@@ -427,6 +427,54 @@ LENS_API lens_status lens_op_attention_window(const uint16_t* q, const uint16_t*
                                               int left, int right, int sinks, float scale, uint16_t* out,
                                               void* stream);
 
+/* The arguments of the four operations in one block, for bindings that pay for every argument
+ * they pass; the fields are the arguments of the same names, in their order.  A NULL block is
+ * INVALID_ARG. */
+typedef struct lens_quantize_f8_args {
+  const void* x;
+  int x_type;
+  int64_t rows, k;
+  int block_rows;
+  uint8_t* codes;
+  float* scales;
+  void* stream;
+} lens_quantize_f8_args;
+typedef struct lens_gemm_f8_args {
+  const uint8_t* A;
+  const float* a_scales;
+  const uint8_t* W;
+  const float *w_scales, *bias;
+  void* C;
+  int c_type, M, N, K;
+  void* stream;
+} lens_gemm_f8_args;
+typedef struct lens_sandwich_norm_args {
+  const float* h;
+  const void* y;
+  int y_type, M, D, rows_per_batch;
+  const float *post_gain, *gate, *pre_gain, *shift, *scale;
+  int64_t mod_stride;
+  float residual_scale, eps;
+  float* h_out;
+  void* out;
+  int out_type;
+  float* out_scales;
+  void* stream;
+} lens_sandwich_norm_args;
+typedef struct lens_attention_window_args {
+  const uint16_t *q, *k, *v;
+  int B, heads, kv_heads, n_q, n_kv;
+  const int *q_start, *kv_len;
+  int left, right, sinks;
+  float scale;
+  uint16_t* out;
+  void* stream;
+} lens_attention_window_args;
+LENS_API lens_status lens_op_quantize_f8_block(const lens_quantize_f8_args* args);
+LENS_API lens_status lens_op_gemm_f8_block(const lens_gemm_f8_args* args);
+LENS_API lens_status lens_op_sandwich_norm_block(const lens_sandwich_norm_args* args);
+LENS_API lens_status lens_op_attention_window_block(const lens_attention_window_args* args);
+
 /* Euler step with optional CFG on tokens: x -= dt * (vu + g (vc - vu)), or
  * x -= dt * vc when v_uncond is NULL.  x, v_cond, v_uncond dev fp32 [n]. */
 LENS_API lens_status lens_op_euler_cfg(float* x, const float* v_cond, const float* v_uncond, int64_t n,

@@ -129,3 +129,35 @@ def test_operations_on_several_streams_at_once():
         torch.cuda.synchronize()
         for (_, out), w in zip(jobs, want):
             assert torch.equal(out, w)
+
+
+def test_the_forms_with_single_arguments_give_the_same_bits():
+    lib, M, D = L.load_library(), 40, 400
+    rng = np.random.default_rng(4)
+    x, h = (torch.from_numpy(rng.standard_normal((M, D)).astype(np.float32)).cuda() for _ in range(2))
+    st = torch.cuda.current_stream().cuda_stream
+
+    def outputs():
+        return (torch.empty((M, D), dtype=torch.uint8, device="cuda"), torch.empty((4, M), device="cuda"),
+                torch.empty((M, D), device="cuda"), torch.empty((M, D), dtype=torch.bfloat16, device="cuda"),
+                torch.empty((M, 48), device="cuda"), torch.empty((1, M, 320), dtype=torch.bfloat16, device="cuda"))
+
+    a, b = outputs(), outputs()
+    w, ws = torch.empty((48, D), dtype=torch.uint8, device="cuda"), torch.empty((4, 1), device="cuda")
+    q = x[:, :320].reshape(M, 5, 64).transpose(0, 1).contiguous().to(torch.bfloat16)
+    L.lens_op_quantize_f8(h[:, :48].t().contiguous().repeat(1, 10), L.LENS_F32, 48, D, 128, w, ws)
+    L.lens_op_quantize_f8(x, L.LENS_F32, M, D, 1, a[0], a[1])
+    L.lens_op_sandwich_norm(h, x, L.LENS_F32, M, D, M, None, None, h[0], x[1], x[2], 0, 0.5, 1e-6, a[2], a[3], L.LENS_BF16)
+    L.lens_op_gemm_f8(a[0], a[1], w, ws, None, a[4], L.LENS_F32, M, 48, D)
+    L.lens_op_attention_window(q, q, q, 1, 5, 5, M, M, None, None, 7, 3, 2, 0.125, a[5])
+    assert lib.lens_op_quantize_f8(x.data_ptr(), 0, M, D, 1, b[0].data_ptr(), b[1].data_ptr(), st) == 0
+    assert lib.lens_op_sandwich_norm(h.data_ptr(), x.data_ptr(), 0, M, D, M, None, None, h[0].data_ptr(),
+                                     x[1].data_ptr(), x[2].data_ptr(), 0, 0.5, 1e-6, b[2].data_ptr(), b[3].data_ptr(),
+                                     1, None, st) == 0
+    assert lib.lens_op_gemm_f8(b[0].data_ptr(), b[1].data_ptr(), w.data_ptr(), ws.data_ptr(), None, b[4].data_ptr(), 0,
+                               M, 48, D, st) == 0
+    assert lib.lens_op_attention_window(q.data_ptr(), q.data_ptr(), q.data_ptr(), 1, 5, 5, M, M, None, None, 7, 3, 2,
+                                        0.125, b[5].data_ptr(), st) == 0
+    torch.cuda.synchronize()
+    for one, other in zip(a, b):
+        assert torch.equal(one, other)

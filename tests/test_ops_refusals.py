@@ -102,3 +102,52 @@ def test_binding_refuses_modulation_rows_of_another_device_or_not_dense():
         with pytest.raises(binding.LensError) as ei:
             binding._rows("norm", dev, bad)
         assert ei.value.status == BAD
+
+
+# valid arguments of each operation (never called as they are: the pointers are made up)
+VALID = {
+    "lens_op_quantize_f8": [16, 0, 4, 128, 1, 16, 16, 0],
+    "lens_op_gemm_f8": [16, 16, 16, 16, 16, 16, 0, 4, 32, 128, 0],
+    "lens_op_sandwich_norm": [16, 16, 1, 4, 128, 4, 16, 16, 16, 16, 16, 128, 1.0, 1e-6, 16, 16, 2, 16, 0],
+    "lens_op_attention_window": [16, 16, 16, 2, 4, 2, 5, 9, 0, 0, 3, 0, 1, 0.125, 16, 0],
+}
+# (argument, value, status): one wrong value for every argument that is looked at
+WRONG = {
+    "lens_op_quantize_f8": [(0, 8, BAD), (1, 2, BAD), (2, 2 ** 40, SHAPE), (3, 2 ** 40, SHAPE), (4, 3, BAD), (5, 8, BAD),
+                            (6, 2, BAD)],
+    "lens_op_gemm_f8": [(0, 8, BAD), (1, 2, BAD), (2, 8, BAD), (3, 2, BAD), (4, 2, BAD), (5, 8, BAD), (6, 2, BAD),
+                        (7, 0, SHAPE), (8, 24, SHAPE), (9, 24, SHAPE)],
+    "lens_op_sandwich_norm": [(0, 8, BAD), (1, 8, BAD), (2, 2, BAD), (3, 0, SHAPE), (4, 24, SHAPE), (5, 0, SHAPE),
+                              (6, 8, BAD), (7, 8, BAD), (8, 8, BAD), (9, 8, BAD), (10, 8, BAD), (11, 6, SHAPE),
+                              (12, float("inf"), BAD), (13, 0.0, BAD), (14, 8, BAD), (15, 8, BAD), (16, 0, BAD),
+                              (17, 2, BAD)],
+    "lens_op_attention_window": [(0, 8, BAD), (1, 8, BAD), (2, 8, BAD), (3, 65, SHAPE), (4, 5, SHAPE), (5, 3, SHAPE),
+                                 (6, 0, SHAPE), (7, 0, SHAPE), (10, -2, BAD), (11, -2, BAD), (12, -1, BAD),
+                                 (13, 0.0, BAD), (14, 8, BAD)],
+}
+
+
+@pytest.mark.parametrize("name", sorted(VALID))
+def test_argument_blocks_hold_the_arguments_in_order(lib, name):
+    """Each wrong argument alone is refused with its status by both forms, and no block by a NULL."""
+    for at, value, status in WRONG[name]:
+        args = list(VALID[name])
+        args[at] = value
+        assert getattr(lib, name)(*args) == status, (at, value)
+        assert lib.f8_blocks[name](binding._BLOCKS[name].pack(*args)) == status, (at, value)
+    assert lib.f8_blocks[name](None) == BAD
+
+
+def test_argument_blocks_hold_the_lengths(lib):
+    for at in (8, 9):
+        args, bad = list(VALID["lens_op_attention_window"]), (ctypes.c_int * 2)(0, -1)
+        args[at] = ctypes.addressof(bad)
+        assert lib.f8_blocks["lens_op_attention_window"](
+            binding._BLOCKS["lens_op_attention_window"].pack(*args)) == SHAPE
+
+
+def test_binding_refuses_numbers_that_do_not_fit():
+    for args in ([16, 0, 4, 128, 2 ** 40, 16, 16, 0], [16, 0, 2 ** 70, 128, 1, 16, 16, 0], [16, 0.5, 4, 128, 1, 16, 16, 0]):
+        with pytest.raises(binding.LensError) as ei:
+            binding._run_block("lens_op_quantize_f8", *args)
+        assert ei.value.status == BAD
