@@ -25,6 +25,7 @@ struct WindowArgs {
   int heads, kv_heads, n_q, n_kv;
   int left, right, sinks;
   float scale_log2;
+  uint32_t per_group;      // 2^32 / (heads / kv_heads), rounded up (0 for 1): the few rows' division
 };
 struct RowSpans {
   int start[kMaxRows];   // position of the first query
@@ -110,17 +111,21 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
   const int rank = blockIdx.x % splits, tile = blockIdx.x / splits, hk = blockIdx.y, b = blockIdx.z;
   const int group = a.heads / a.kv_heads, rows = a.n_q * group, row0 = tile * 16;
   const int start = spans.start[b], len = spans.len[b];
+  // query of a row, exact since rows (48 queries of 1024 heads at most) times group stay below
+  // 2^32, and the head in its group
+  auto query = [&](int row) { return a.per_group ? (int)__umulhi(row, a.per_group) : row; };
+  auto member = [&](int row) { return row - query(row) * group; };
   if constexpr (splits > 1) cluster_arrive();             // waited for before the others are written to
   grid_dependency_sync();
 
   // this thread's rows g and g + 8 (a row past the last repeats it and is not stored)
   const int r_lo = min(row0 + g, rows - 1), r_hi = min(row0 + g + 8, rows - 1);
-  const KeyRange k_lo = key_range(a, start + r_lo / group, len), k_hi = key_range(a, start + r_hi / group, len);
+  const KeyRange k_lo = key_range(a, start + query(r_lo), len), k_hi = key_range(a, start + query(r_hi), len);
   uint32_t q[4][4];
   {
     const __nv_bfloat16* base = a.q + ((int64_t)b * a.heads + (int64_t)hk * group) * a.n_q * 64;
-    const __nv_bfloat16* p0 = base + ((int64_t)(r_lo % group) * a.n_q + r_lo / group) * 64 + 8 * c;
-    const __nv_bfloat16* p1 = base + ((int64_t)(r_hi % group) * a.n_q + r_hi / group) * 64 + 8 * c;
+    const __nv_bfloat16* p0 = base + ((int64_t)member(r_lo) * a.n_q + query(r_lo)) * 64 + 8 * c;
+    const __nv_bfloat16* p1 = base + ((int64_t)member(r_hi) * a.n_q + query(r_hi)) * 64 + 8 * c;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint4 x = *reinterpret_cast<const uint4*>(p0 + 32 * u), y = *reinterpret_cast<const uint4*>(p1 + 32 * u);
@@ -129,8 +134,8 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
     }
   }
   // the keys any row of the tile attends: [0, sink) and [lo, hi), counted on through both
-  const KeyRange first = key_range(a, start + row0 / group, len);
-  const KeyRange last = key_range(a, start + min(row0 + 15, rows - 1) / group, len);
+  const KeyRange first = key_range(a, start + query(row0), len);
+  const KeyRange last = key_range(a, start + query(min(row0 + 15, rows - 1)), len);
   const int hi = last.hi, lo = min(first.lo, hi), sink = min(last.s, lo);
   const int count = sink + hi - lo;
   const uint4 *kp = reinterpret_cast<const uint4*>(a.k + ((int64_t)b * a.kv_heads + hk) * a.n_kv * 64),
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
     // a row with no attended key (or only scores of -inf) writes zeros
     y = sum == 0.f ? 0.f : y / sum;
     if (row0 + r < rows) {
-      const int i = (row0 + r) / group, h = hk * group + (row0 + r) % group;
+      const int i = query(row0 + r), h = hk * group + member(row0 + r);
       a.out[(((int64_t)b * a.n_q + i) * a.heads + h) * 64 + d] = __float2bfloat16_rn(y);
       if (!isfinite(y)) s_redo[r] = 1;
     }
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
   // out non-finite are done again from their attended keys alone.
   for (int r = rank * share + warp; r < (rank + 1) * share; r += WARPS)
     if (s_redo[r])
-      attend_row(a, b, hk * group + (row0 + r) % group, (row0 + r) / group, start + (row0 + r) / group, len);
+      attend_row(a, b, hk * group + member(row0 + r), query(row0 + r), start + query(row0 + r), len);
 }
 
 cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, int sms, cudaStream_t st) {
@@ -888,7 +893,8 @@ extern "C" lens_status lens_op_attention_window(const uint16_t* q, const uint16_
   const WindowArgs a{reinterpret_cast<const __nv_bfloat16*>(q), reinterpret_cast<const __nv_bfloat16*>(k),
                      reinterpret_cast<const __nv_bfloat16*>(v), reinterpret_cast<__nv_bfloat16*>(out), heads, kv_heads,
                      n_q, n_kv, left < 0 || left > kMaxPos ? kMaxPos : left,
-                     right < 0 || right > kMaxPos ? kMaxPos : right, sinks, scale * 1.4426950408889634f};
+                     right < 0 || right > kMaxPos ? kMaxPos : right, sinks, scale * 1.4426950408889634f,
+                     heads > kv_heads ? (uint32_t)(((1ull << 32) + heads / kv_heads - 1) / (heads / kv_heads)) : 0u};
   cudaStream_t st = (cudaStream_t)stream;
   const int sms = device_sms();
   if (few_rows(a, B, sms)) return launch_few(a, spans, B, sms, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
