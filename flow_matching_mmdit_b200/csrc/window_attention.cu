@@ -87,7 +87,7 @@ __device__ __forceinline__ void attend_row(const WindowArgs& a, int b, int h, in
 // 64 columns are dealt to the MMA's k slots so that a thread's eight consecutive columns
 // fill its slots of two steps; for O = P V output column n of MMA j is column 8 n + j, so
 // that a thread's eight consecutive columns of a V row feed the eight MMAs.
-constexpr int kFewStep = 32, kFewMaxSplit = 8;
+constexpr int kFewStep = 32, kFewMaxSplit = 8, kFewLongSplit = 16;   // 8 is the portable cluster size
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -313,6 +313,34 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
       attend_row(a, b, hk * group + member(row0 + r), query(row0 + r), start + query(row0 + r), len);
 }
 
+// Clusters of kFewLongSplit CTAs that the current device runs at a time (0: none), looked up once
+// per device.
+int long_clusters() {
+  constexpr int DEVICES = 64;
+  static std::atomic<int> known[DEVICES];               // one more than the number
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= DEVICES) return 0;
+  if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n - 1;
+  const auto kernel = window_attention_few_kernel<kFewLongSplit, 8>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kFewLongSplit);
+  cfg.blockDim = dim3(256);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kFewLongSplit;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();                                  // not a failure of the call: eight CTAs will do
+    n = 0;
+  }
+  known[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, int sms, cudaStream_t st) {
   const int rows = a.n_q * (a.heads / a.kv_heads);
   // the most keys a tile may read
@@ -330,6 +358,12 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, int sm
   // past two steps a warp: eight warps a CTA (8192 keys, 32 heads on 8: 10.2 us for 15.5;
   // 1028 keys: 15.5 for 8.0, fewer CTAs fit an SM)
   const bool wide = splits == kFewMaxSplit && keys > 2 * kFewMaxSplit * 4 * kFewStep;
+  // and sixteen CTAs where so few tiles leave SMs idle, or the keys are many more (one query, us
+  // for sixteen / eight CTAs: 4 tiles, 2100 keys 5.4 / 6.3, 8192 keys 7.3 / 10.5, 131072 keys 69
+  // / 131; 8 tiles, 2100 keys 6.9 / 6.3, 8192 keys 9.6 / 10.6, 131072 keys 90 / 132)
+  if (wide && (2 * kFewLongSplit * tiles <= sms || (kFewLongSplit * tiles <= sms && keys > 4096)) &&
+      tiles <= long_clusters())
+    splits = kFewLongSplit;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((rows + 15) / 16 * splits, a.kv_heads, B);
   cfg.blockDim = dim3(wide ? 256 : 128);
@@ -343,6 +377,7 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, int sm
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  if (splits == kFewLongSplit) return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<kFewLongSplit, 8>, a, spans);
   if (wide) return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<8, 8>, a, spans);
   switch (splits) {
     case 1: return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<1, 4>, a, spans);

@@ -109,6 +109,14 @@ def test_few_queries_against_a_cache(H, Hk, nq, nkv, left, sinks):
     check(run(q, k, v, start, length, left, 0, sinks), q, k, v, start, length, left, 0, sinks)
 
 
+@pytest.mark.parametrize("H,Hk", [(1, 1), (16, 4), (32, 8), (9, 9), (12, 12)])
+@pytest.mark.parametrize("nq,nkv", [(1, 2500), (3, 9001), (1, 20000)])
+def test_few_queries_against_all_of_a_long_cache(H, Hk, nq, nkv):
+    q, k, v = make(1, H, Hk, nq, nkv, H + nkv)
+    check(run(q, k, v, [nkv - nq], None, -1, 0, 0), q, k, v, [nkv - nq], None, -1, 0, 0)
+    check(run(q, k, v, [nkv - nq], [nkv - 70], -1, 0, 5), q, k, v, [nkv - nq], [nkv - 70], -1, 0, 5)
+
+
 @pytest.mark.parametrize("B,H,Hk,nkv", [(40, 24, 24, 700), (64, 8, 8, 1100), (20, 16, 4, 2300)])
 def test_one_query_in_large_batches(B, H, Hk, nkv):
     """Enough tiles for the keys to be split over fewer CTAs, down to one."""
