@@ -33,7 +33,7 @@ EXPORTS = [
     "lens_sampler_update", "lens_sampler_finish", "lens_op_quantize_w4", "lens_op_gemm_w4",
     "lens_op_quantize_f8", "lens_op_gemm_f8", "lens_op_sandwich_norm", "lens_op_attention_window",
     "lens_op_quantize_f8_block", "lens_op_gemm_f8_block", "lens_op_sandwich_norm_block",
-    "lens_op_attention_window_block",
+    "lens_op_attention_window_block", "lens_op_sync", "lens_op_debug_raise_abort",
 ]
 
 # lens_dtype
@@ -126,6 +126,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lens_op_gemm_f8": (I, [P, P, P, P, P, P, I, I, I, I, P]),
         "lens_op_sandwich_norm": (I, [P, P, I, I, I, I, P, P, P, P, P, L, F, F, P, P, I, P, P]),
         "lens_op_attention_window": (I, [P, P, P, I, I, I, I, I, P, P, I, I, I, F, P, P]),
+        "lens_op_sync": (I, [P]),
+        "lens_op_debug_raise_abort": (I, [P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -334,6 +336,15 @@ def lens_dit_op_text_input(h: LensDit, txt, B: int, n_txt: int, c, stream=None) 
 
 
 # ---------------------------------------------------------------- single ops
+def lens_op_sync(stream=None) -> None:
+    """Wait for the work on the stream; raises LENS_ERR_TIMEOUT, once, when a handle-free operation gave up."""
+    _check(load_library().lens_op_sync(_stream(stream)), "lens_op_sync")
+
+
+def lens_op_debug_raise_abort(stream=None) -> None:
+    _check(load_library().lens_op_debug_raise_abort(_stream(stream)), "lens_op_debug_raise_abort")
+
+
 def lens_op_noise_tokens(seed: int, B: int, grid_h: int, grid_w: int, tokens, stream=None) -> None:
     _check(load_library().lens_op_noise_tokens(seed, B, grid_h, grid_w, _ptr(tokens), _stream(stream)),
            "lens_op_noise_tokens")

@@ -131,8 +131,8 @@ extern "C" lens_status lens_op_gemm_f8(const uint8_t* A, const float* a_scales, 
     return LENS_ERR_SHAPE;
   if (!aligned16(A) || !aligned16(W) || !aligned16(C) || !aligned4(a_scales) || !aligned4(w_scales) || !aligned4(bias))
     return LENS_ERR_INVALID_ARG;
-  int* err = op_err_ptr();
-  if (!err) return LENS_ERR_CUDA;
+  int* err = nullptr;
+  if (const lens_status s = op_abort_flag(&err)) return s;
   const F8Gemm g{A, W, a_scales, w_scales, bias, C, c_type == LENS_BF16, M, N, K};
   return launch_gemm_f8(g, err, device_sms(), (cudaStream_t)stream) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
 }

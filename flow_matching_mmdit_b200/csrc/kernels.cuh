@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "lens_dit.h"
 #include "ptx.cuh"
 
 namespace lens {
@@ -34,8 +35,9 @@ struct TextLengths {
 };
 
 // lens_dit.cu: the abort flag that the handle-free operations share on the current device
-// (nullptr when it cannot be had), and the current device's number of SMs
-int* op_err_ptr();
+// (LENS_ERR_TIMEOUT while it is known to be raised, LENS_ERR_CUDA when it cannot be had), and
+// the current device's number of SMs
+lens_status op_abort_flag(int** err);
 int device_sms();
 
 // attention.cu (txt_len == nullptr: every text key is valid)

@@ -7,6 +7,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <mutex>
 #include <string>
 #include <unordered_map>
 #include <vector>
@@ -221,19 +222,61 @@ static GemmProblem base_problem(int M, int N, int K) {
   return p;
 }
 
-// ============================================================ module-level error flag
-// Used by the handle-free op entry points.
-__device__ int g_op_err;
-int* lens::op_err_ptr() {
-  static std::atomic<int*> known[kCachedDevices];
+// ============================================================ module-level abort flag
+// Shared by the handle-free entry points on a device: raised by a kernel's expired wait,
+// reported by every later call that uses it and by lens_op_sync, which clears it.
+__device__ AbortFlag g_op_abort;
+
+namespace {
+struct OpAbort {
+  std::atomic<AbortFlag*> flag;   // on the device; set last
+  volatile int* host;             // the word set with it
+};
+
+// The current device's, or null.  The first call on a device pins the host word and stores
+// its address beside the flag, aside from any capture that a thread may have open.
+OpAbort* op_abort() {
+  static OpAbort known[kCachedDevices];
+  static std::mutex mutex;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-  const bool cached = dev >= 0 && dev < kCachedDevices;
-  int* p = cached ? known[dev].load(std::memory_order_relaxed) : nullptr;
-  if (p) return p;
-  if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_op_err) != cudaSuccess) return nullptr;
-  if (cached) known[dev].store(p, std::memory_order_relaxed);
-  return p;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kCachedDevices) return nullptr;
+  OpAbort& a = known[dev];
+  if (a.flag.load(std::memory_order_acquire)) return &a;
+  const std::lock_guard<std::mutex> lock(mutex);
+  if (a.flag.load(std::memory_order_relaxed)) return &a;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+  void *flag = nullptr, *host = nullptr, *mapped = nullptr;
+  cudaStream_t st = nullptr;
+  bool ok = cudaGetSymbolAddress(&flag, g_op_abort) == cudaSuccess &&
+            cudaHostAlloc(&host, sizeof(int), cudaHostAllocMapped) == cudaSuccess &&
+            cudaHostGetDevicePointer(&mapped, host, 0) == cudaSuccess &&
+            cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking) == cudaSuccess;
+  if (ok) {
+    *static_cast<int*>(host) = 0;
+    ok = cudaMemcpyAsync(&static_cast<AbortFlag*>(flag)->host, &mapped, sizeof(mapped), cudaMemcpyHostToDevice, st) ==
+             cudaSuccess &&
+         cudaStreamSynchronize(st) == cudaSuccess;
+  }
+  if (st) cudaStreamDestroy(st);
+  if (!ok) {
+    if (host) cudaFreeHost(host);
+    cudaGetLastError();
+  }
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (!ok) return nullptr;
+  a.host = static_cast<int*>(host);
+  a.flag.store(static_cast<AbortFlag*>(flag), std::memory_order_release);
+  return &a;
+}
+}  // namespace
+
+lens_status lens::op_abort_flag(int** err) {
+  OpAbort* a = op_abort();
+  if (!a) return LENS_ERR_CUDA;
+  if (*a->host) return LENS_ERR_TIMEOUT;
+  *err = &a->flag.load(std::memory_order_relaxed)->raised;
+  return LENS_OK;
 }
 
 // ============================================================ weight loading
@@ -562,7 +605,7 @@ static size_t layout_workspace(lens_dit* h, Bump& b) {
   h->mod = b.take<float>(Tm * h->modw);
   h->rope = b.take<float2>(N * 32);
   h->cfgpart = b.take<double>(Bm * kCfgNormParts * 2);
-  h->err = b.take<int>(1);
+  h->err = &b.take<AbortFlag>(1)->raised;
   return b.off;
 }
 
@@ -988,7 +1031,7 @@ lens_status lens_dit_create(const lens_dit_config* cfg, const lens_weight* w, in
     h->wstage = nullptr;
   }
   if (s == LENS_OK) s = make_weight_maps(h);
-  if (s == LENS_OK && cudaMemsetAsync(h->err, 0, sizeof(int), (cudaStream_t)stream) != cudaSuccess)
+  if (s == LENS_OK && cudaMemsetAsync(h->err, 0, sizeof(AbortFlag), (cudaStream_t)stream) != cudaSuccess)
     s = LENS_ERR_CUDA;
   if (s == LENS_OK && cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) s = LENS_ERR_CUDA;
   if (s != LENS_OK) {
@@ -1028,6 +1071,29 @@ lens_status lens_dit_sync(lens_dit* h, void* stream) {
     return LENS_ERR_TIMEOUT;
   }
   return LENS_OK;
+}
+
+lens_status lens_op_debug_raise_abort(void* stream) {
+  OpAbort* a = op_abort();
+  if (!a) return LENS_ERR_CUDA;
+  AbortFlag* flag = a->flag.load(std::memory_order_relaxed);
+  LENS_CUDA(cudaMemsetAsync(&flag->raised, 1, 1, (cudaStream_t)stream));
+  LENS_CUDA(cudaMemcpyAsync(const_cast<int*>(a->host), &flag->raised, sizeof(int), cudaMemcpyDeviceToHost,
+                            (cudaStream_t)stream));
+  return LENS_OK;
+}
+
+lens_status lens_op_sync(void* stream) {
+  LENS_CUDA(cudaStreamSynchronize((cudaStream_t)stream));
+  OpAbort* a = op_abort();
+  if (!a) return LENS_ERR_CUDA;
+  if (!*a->host) return LENS_OK;
+  // the operations of other streams may have given up too, and must not outlast the flag
+  LENS_CUDA(cudaDeviceSynchronize());
+  LENS_CUDA(cudaMemset(&a->flag.load(std::memory_order_relaxed)->raised, 0, sizeof(int)));
+  LENS_CUDA(cudaDeviceSynchronize());
+  *a->host = 0;
+  return LENS_ERR_TIMEOUT;
 }
 
 static lens_status check_sizes(lens_dit* h, int B, int gh, int gw, int n_txt) {
@@ -1336,8 +1402,8 @@ lens_status lens_op_gemm_w4(const uint16_t* A, const uint8_t* codes, const uint3
   if (!encode_tmap_bf16(&ta, A, M, K, K, 128) || !encode_tmap_w4_codes(&tq, codes, N, K, bn) ||
       !encode_tmap_w4_scales(&ts, scales, N, K, bn) || !encode_tmap_out(&tc, C, 4, M, N, N))
     return LENS_ERR_INVALID_ARG;
-  int* err = op_err_ptr();
-  if (!err) return LENS_ERR_CUDA;
+  int* err = nullptr;
+  if (const lens_status s = op_abort_flag(&err)) return s;
   GemmArgs a = make_args(err);
   a.num_problems = 1;
   a.p[0] = base_problem(M, N, K);
@@ -1360,8 +1426,8 @@ lens_status lens_op_gemm_bf16(const uint16_t* A, const uint16_t* Bm, const float
     return LENS_ERR_INVALID_ARG;
   CUtensorMap tc;
   if (!encode_tmap_out(&tc, C, 4, M, N, N)) return LENS_ERR_INVALID_ARG;
-  int* err = op_err_ptr();
-  if (!err) return LENS_ERR_CUDA;
+  int* err = nullptr;
+  if (const lens_status s = op_abort_flag(&err)) return s;
   GemmArgs a = make_args(err);
   a.num_problems = 1;
   a.p[0] = base_problem(M, N, K);
@@ -1402,8 +1468,8 @@ lens_status lens_op_attention_masked(const uint16_t* q, const uint16_t* k, const
       if (txt_len[b] == 0) return LENS_ERR_SHAPE;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
     return LENS_ERR_INVALID_ARG;
-  int* err = op_err_ptr();
-  if (!err) return LENS_ERR_CUDA;
+  int* err = nullptr;
+  if (const lens_status s = op_abort_flag(&err)) return s;
   LENS_CUDA(launch_joint_attention(
       reinterpret_cast<const __nv_bfloat16*>(q), reinterpret_cast<const __nv_bfloat16*>(k),
       reinterpret_cast<const __nv_bfloat16*>(v), B, kHeads, n_txt, n_img, reinterpret_cast<__nv_bfloat16*>(out_txt),

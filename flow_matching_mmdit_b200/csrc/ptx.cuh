@@ -14,6 +14,20 @@ namespace lens {
 // and leave too.  A kernel never traps.
 constexpr unsigned long long kWaitLimitNs = 2000ull * 1000ull * 1000ull;   // 2 s
 
+// An abort flag: the word that kernels poll (their `err`) and, where there is one, a host
+// word that is set with it, so that the host can see it without waiting for the device.
+struct AbortFlag {
+  int raised;
+  int unused;
+  int* host;       // mapped host memory, or null
+};
+
+__device__ __forceinline__ void raise_abort(int* err) {
+  if (atomicCAS(err, 0, 1) != 0) return;
+  int* host = *reinterpret_cast<int* volatile*>(&reinterpret_cast<AbortFlag*>(err)->host);
+  if (host) *reinterpret_cast<volatile int*>(host) = 1;
+}
+
 __device__ __forceinline__ unsigned long long globaltimer_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
@@ -87,7 +101,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
     if ((it & 255u) == 0) {
       if (*reinterpret_cast<volatile int*>(err) != 0) return false;
       if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        atomicCAS(err, 0, 1);
+        raise_abort(err);
         return false;
       }
     }
@@ -118,7 +132,7 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, 
     if ((it & 15u) == 0) {
       if (*reinterpret_cast<volatile int*>(err) != 0) return false;
       if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        atomicCAS(err, 0, 1);
+        raise_abort(err);
         return false;
       }
     }

@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   Bars& bar = *reinterpret_cast<Bars*>(sm + OFF_BAR);
   // 128-byte swizzled tiles need this alignment, and there is no room left to round up
   if (smem_u32(sm) & 1023) {
-    if (threadIdx.x == 0) atomicCAS(err, 0, 1);
+    if (threadIdx.x == 0) raise_abort(err);
     return;
   }
 
@@ -933,8 +933,8 @@ extern "C" lens_status lens_op_attention_window(const uint16_t* q, const uint16_
   cudaStream_t st = (cudaStream_t)stream;
   const int sms = device_sms();
   if (few_rows(a, B, sms)) return launch_few(a, spans, B, sms, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
-  int* err = op_err_ptr();
-  if (!err) return LENS_ERR_CUDA;
+  int* err = nullptr;
+  if (const lens_status s = op_abort_flag(&err)) return s;
   return launch_many(a, spans, B, err, st) == cudaSuccess ? LENS_OK : LENS_ERR_CUDA;
 }
 

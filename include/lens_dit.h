@@ -23,7 +23,8 @@
  *   - All GPU work is enqueued on `stream` (a cudaStream_t, NULL = legacy default
  *     stream).  Argument errors return synchronously and enqueue nothing.  Errors
  *     from kernels (including the device watchdog on internal waits) surface
- *     through lens_dit_sync() or the next call.
+ *     through lens_dit_sync(), for the handle-free operations lens_op_sync(), or the
+ *     next call.
  *   - No entry point falls back to the CPU.  A handle is used by one stream at a
  *     time.  Forward and sample calls allocate nothing: the handle's workspace is
  *     sized at create time from the config's max_* fields.
@@ -269,8 +270,27 @@ LENS_API const char* lens_status_string(lens_status s);
 
 /* ---------------------------------------------------------------------------
  * Single-operation entry points (the same kernels the denoiser runs), for
- * parity tests of each step.  Handle-free unless stated; no allocation.
+ * parity tests of each step.  Handle-free unless stated; no device allocation.
+ *
+ * lens_op_gemm_bf16, lens_op_gemm_w4, lens_op_attention(_masked), lens_op_gemm_f8
+ * and lens_op_attention_window share one abort flag a device.  When an internal
+ * wait of one of them expires (2 s; no valid call does that), it and those running
+ * beside it on any stream leave without finishing, so their outputs are not valid,
+ * and every later call of them on the device returns LENS_ERR_TIMEOUT without
+ * enqueueing anything until lens_op_sync has reported it.  Replays of captured
+ * graphs pass no such check: call lens_op_sync after them.  The first of these calls
+ * on a device pins one word of host memory.
  * ------------------------------------------------------------------------- */
+
+/* Wait for the work on `stream` and report what the handle-free operations of the
+ * current device met: CUDA, or TIMEOUT when one of them has given up since the last
+ * report.  A TIMEOUT waits for all work of the device and clears the flag.  Not
+ * during a stream capture. */
+LENS_API lens_status lens_op_sync(void* stream);
+
+/* Test hook for their failure path: raise the flag on `stream`, as an expired wait
+ * would.  Errors: CUDA. */
+LENS_API lens_status lens_op_debug_raise_abort(void* stream);
 
 /* Seeded N(0,1) latent noise straight into patch tokens (noise definition as in
  * lens_sample_euler; patchify: token (i, j) of row-major order, feature
