@@ -435,6 +435,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             d32[4 * g] = pack_bf16x2(o[4 * g + 2 * rr] * inv, o[4 * g + 2 * rr + 1] * inv);
         }
       }
+    } else {
+      report_abort(err);
     }
   }
   tc_fence_before();

@@ -289,7 +289,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i < PIECE / 32; ++i) tmem_ld32(at + PIECE * (c + 1) + 32 * i, r[i]);
         }
       }
-      if (!ok) break;
+      if (!ok) {
+        report_abort(a.err);
+        break;
+      }
       int tm, tn;
       tile_of(a, t, tm, tn);
       const int row0 = tm * 256 + 128 * (int)rank + quarter * 32;
@@ -636,6 +639,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             static_cast<float*>(p.g.C)[to] = o[i];
         }
     }
+  } else if (warp >= 4) {
+    report_abort(p.err);
   }
   if (warp == 1) {
     tc_fence_after();

@@ -483,7 +483,10 @@ __global__ void __launch_bounds__(192, 1)
       const int row0 = m0 + quarter * 32;
       float4 pre[16];
       epilogue_prefetch<BN, EPI>(args.p[pi], row0 + lane, n0, 0, 1, pre);
-      if (!mbar_wait(&tfull[acc], use & 1, args.err)) break;
+      if (!mbar_wait(&tfull[acc], use & 1, args.err)) {
+        report_abort(args.err);
+        break;
+      }
       tc_fence_after();
       const uint32_t taddr = tmem_base + (uint32_t(quarter * 32) << 16) + acc * BN;
       epilogue_tile<BN, EPI>(args.p[pi], pi ? &tmC1 : &tmC0, row0 + lane, row0, n0, taddr, slots, slot,
@@ -792,7 +795,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<BN, EPI>::T
       const int row0 = m0 + 128 * (int)rank + quarter * 32;
       float4 pre[16];
       epilogue_prefetch<BN, EPI>(args.p[pi], row0 + lane, n0, part, C::EPI_PARTS, pre, width);
-      if (!mbar_wait(&tfull[acc], use & 1, args.err)) break;
+      if (!mbar_wait(&tfull[acc], use & 1, args.err)) {
+        report_abort(args.err);
+        break;
+      }
       tc_fence_after();
       const uint32_t taddr = tmem_base + (uint32_t(quarter * 32) << 16) + acc * BN;
       epilogue_tile<BN, EPI, C::EPI_SLOTS>(args.p[pi], pi ? &tmC1 : &tmC0, row0 + lane, row0, n0, taddr, slots,

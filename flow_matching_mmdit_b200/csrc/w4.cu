@@ -308,7 +308,10 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       w4_decode<MH>(args, t, BN, pi, m0, n0);
       const uint32_t acc = li & 1;
       const uint32_t use = li >> 1;
-      if (!mbar_wait(&tfull[acc], use & 1, args.err)) break;
+      if (!mbar_wait(&tfull[acc], use & 1, args.err)) {
+        report_abort(args.err);
+        break;
+      }
       tc_fence_after();
 #pragma unroll 1
       for (int h = 0; h < MH; ++h) {

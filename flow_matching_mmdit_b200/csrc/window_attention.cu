@@ -423,6 +423,7 @@ struct Bars {
   uint64_t pv_done;      // MMA -> softmax: O += P V finished
   uint64_t drain[2];     // each MMA issuer's own completion after an abort
   uint32_t tmem_slot;
+  uint32_t aborted;      // the softmax has left its loop early
 };
 static_assert(sizeof(Bars) <= 256, "barriers overflow their shared-memory reserve");
 
@@ -479,7 +480,10 @@ __global__ void __launch_bounds__(THREADS, 2)
   Bars& bar = *reinterpret_cast<Bars*>(sm + OFF_BAR);
   // 128-byte swizzled tiles need this alignment, and there is no room left to round up
   if (smem_u32(sm) & 1023) {
-    if (threadIdx.x == 0) raise_abort(err);
+    if (threadIdx.x == 0) {
+      atomicCAS(err, 0, 1);
+      report_abort(err);
+    }
     return;
   }
 
@@ -509,6 +513,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     mbar_init(&bar.pv_done, 1);
     mbar_init(&bar.drain[0], 1);
     mbar_init(&bar.drain[1], 1);
+    bar.aborted = 0;
     fence_mbar_init();
     // this thread is the producer too: its first loads need nobody else's set-up
     grid_dependency_wait();
@@ -813,7 +818,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (__all_sync(0xffffffffu, ok && (nkv == 0 || mbar_wait(&bar.pv_done, (nkv - 1) & 1, err)))) {
+    ok = __all_sync(0xffffffffu, ok && (nkv == 0 || mbar_wait(&bar.pv_done, (nkv - 1) & 1, err)));
+    if (!ok) bar.aborted = 1;
+    if (ok) {
       float o[32];
       if (nkv > 0) {
         tc_fence_after();
@@ -865,6 +872,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   tc_fence_before();
   __syncthreads();
+  if (bar.aborted && threadIdx.x == 0) report_abort(err);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
