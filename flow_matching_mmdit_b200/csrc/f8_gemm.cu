@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             use ^= 1;
           }
         }
-        if (!ok) umma_drain_pair(&drain[odd]);
+        // after an abort the epilogue may not have waited for every block issued here
+        if (!ok || err_raised(a.err)) umma_drain_pair(&drain[odd]);
       }
       __syncwarp();
     } else {
@@ -527,7 +528,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           use ^= 1;
         }
       }
-      if (!ok) umma_drain(&drain[odd]);
+      // after an abort the adding warps may not have waited for every block issued here
+      if (!ok || err_raised(p.err)) umma_drain(&drain[odd]);
     }
     __syncwarp();
   } else if (warp == 3) {

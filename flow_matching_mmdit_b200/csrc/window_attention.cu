@@ -423,7 +423,7 @@ struct Bars {
   uint64_t pv_done;      // MMA -> softmax: O += P V finished
   uint64_t drain[2];     // each MMA issuer's own completion after an abort
   uint32_t tmem_slot;
-  uint32_t aborted;      // the softmax has left its loop early
+  uint32_t aborted;      // the softmax has left without waiting for every MMA
 };
 static_assert(sizeof(Bars) <= 256, "barriers overflow their shared-memory reserve");
 
@@ -533,6 +533,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   const uint32_t tmem = bar.tmem_slot;
   grid_dependency_sync();    // set-up above touched only shared memory and TMEM
 
+  bool drained = false;      // an issuer that has waited for its MMAs
   // 64 scores a softmax thread do not fit an even share of the registers (80): its two
   // warpgroups take over what the first gives up (32 + 2 x 104 = 3 x 80)
   if (warp < 4) {
@@ -576,6 +577,7 @@ __global__ void __launch_bounds__(THREADS, 2)
           umma_commit(&bar.s_full);
           umma_commit(&bar.kv_empty[s]);
         }
+        drained = !ok;
         if (!ok) umma_drain(&bar.drain[0]);   // no S MMA still runs when TMEM is freed
       }
       __syncwarp();
@@ -604,6 +606,7 @@ __global__ void __launch_bounds__(THREADS, 2)
           umma_commit(&bar.pv_done);
           umma_commit(&bar.kv_empty[s]);
         }
+        drained = !ok;
         if (!ok) umma_drain(&bar.drain[1]);   // no P V MMA still runs when TMEM is freed
       }
       __syncwarp();
@@ -872,7 +875,11 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (bar.aborted && threadIdx.x == 0) report_abort(err);
+  if (bar.aborted) {
+    if (threadIdx.x == 0) report_abort(err);
+    if (lane == 0 && nkv > 0 && (warp == 1 || warp == 2) && !drained) umma_drain(&bar.drain[warp - 1]);
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);

@@ -94,6 +94,30 @@ def test_a_call_after_an_abort_reports_it(make, size):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("make,size", FLAGGED)
+def test_kernels_launched_behind_an_abort_leave_and_the_next_are_right(make, size):
+    """Launched before the host sees the flag (or refused, if it already has): each leaves in
+    order, draining what it started, and nothing of it reaches the calls after the report."""
+    call, out = make(*size)
+    call()
+    L.lens_op_sync()
+    want = out.clone()
+    for _ in range(3):
+        L.lens_op_debug_raise_abort()
+        for _ in range(4):
+            try:
+                call()
+            except L.LensError as e:
+                assert e.status == TIMEOUT
+        with pytest.raises(L.LensError) as e:
+            L.lens_op_sync()
+        assert e.value.status == TIMEOUT
+        out.zero_()
+        call()
+        L.lens_op_sync()
+        assert torch.equal(out, want)
+
+
 def test_sync_on_another_stream_reports_it_too():
     side = torch.cuda.Stream()
     L.lens_op_debug_raise_abort(stream=side)
