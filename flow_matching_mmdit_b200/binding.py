@@ -443,12 +443,22 @@ def _whole(where: str, stream, *tensors):
     return out
 
 
-def _rows(where: str, dev: int, x) -> Optional[int]:
-    """Device pointer of a view whose rows are dense (None passes NULL); one of another device is refused."""
+def _rows(where: str, dev: int, x, samples: int = 1, D: int = 0, mod_stride: int = 0) -> Optional[int]:
+    """Device pointer of a view of `samples` dense rows of D values, mod_stride apart (None passes NULL).
+    One of another device, of rows that are not dense, or without those rows at that distance (in a
+    dimension of its own, or anywhere in a contiguous tensor that is long enough) is refused."""
     if x is None:
         return None
     if x.get_device() != dev or x.stride(-1) != 1:
         raise LensError(1, where)
+    if x.size(-1) >= D:
+        if samples <= 1 or mod_stride == 0:
+            return x.data_ptr()
+        for i in range(x.dim() - 1):
+            if x.stride(i) == mod_stride and x.size(i) >= samples:
+                return x.data_ptr()
+    if not x.is_contiguous() or x.numel() < (samples - 1) * mod_stride + D:
+        raise LensError(2, where)
     return x.data_ptr()
 
 
@@ -469,8 +479,10 @@ def lens_op_sandwich_norm(h, y, y_type: int, M: int, D: int, rows_per_batch: int
     where = "lens_op_sandwich_norm"
     ph, py, pp, pq, pho, po, pos, st = _whole(where, stream, h, y, post_gain, pre_gain, h_out, out, out_scales)
     dev = -1 if h is None else h.get_device()
-    _run_block(where, ph, py, y_type, M, D, rows_per_batch, pp, _rows(where, dev, gate) or 0, pq,
-               _rows(where, dev, shift) or 0, _rows(where, dev, scale) or 0, mod_stride, residual_scale, eps, pho, po,
+    samples = -(-M // rows_per_batch) if rows_per_batch > 0 else 1
+    _run_block(where, ph, py, y_type, M, D, rows_per_batch, pp, _rows(where, dev, gate, samples, D, mod_stride) or 0,
+               pq, _rows(where, dev, shift, samples, D, mod_stride) or 0,
+               _rows(where, dev, scale, samples, D, mod_stride) or 0, mod_stride, residual_scale, eps, pho, po,
                out_type, pos, st)
 
 
