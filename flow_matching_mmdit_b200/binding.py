@@ -491,8 +491,11 @@ def lens_op_attention_window(q, k, v, B: int, heads: int, kv_heads: int, n_q: in
                              sinks: int, scale: float, out, stream=None) -> None:
     """q_start and kv_len hold one entry per batch row; a list of another length is refused."""
     # array.array: a tenth of the time a numpy array and its address take
-    qs = None if q_start is None else array("i", q_start)
-    kl = None if kv_len is None else array("i", kv_len)
+    try:
+        qs = None if q_start is None else array("i", q_start)
+        kl = None if kv_len is None else array("i", kv_len)
+    except OverflowError:                        # a length that an int does not hold
+        raise LensError(1, "lens_op_attention_window") from None
     if (qs is not None and len(qs) != B) or (kl is not None and len(kl) != B):
         raise LensError(2, "lens_op_attention_window")
     pq, pk, pv, po, st = _whole("lens_op_attention_window", stream, q, k, v, out)

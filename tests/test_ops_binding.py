@@ -44,3 +44,12 @@ def test_modulation_rows_of_one_sample_and_of_flat_tensors():
     refused(SHAPE, lambda: rows(one, 2, D))
     refused(SHAPE, lambda: rows(one[:-16], 1, 0))
     refused(SHAPE, lambda: rows(torch.zeros(2, D)[:, :-16], 2, D))
+
+
+@pytest.mark.parametrize("at", [0, 1])
+@pytest.mark.parametrize("value", [2 ** 31, -2 ** 31 - 1, 2 ** 70])
+def test_lengths_past_32_bits_are_refused(at, value):
+    lengths = [[0, 0], [8, 8]]
+    lengths[at][1] = value
+    refused(BAD, lambda: binding.lens_op_attention_window(None, None, None, 2, 4, 4, 1, 8, *lengths, 1, 0, 0, 0.125, None,
+                                                          stream=0))
