@@ -36,7 +36,7 @@ struct RowSpans {
 struct KeyRange {
   int s, lo, hi;
 };
-__device__ __forceinline__ KeyRange key_range(const WindowArgs& a, int p, int len) {
+__host__ __device__ __forceinline__ KeyRange key_range(const WindowArgs& a, int p, int len) {
   KeyRange r;
   r.hi = min(p + a.right + 1, len);
   r.lo = max(p - a.left, 0);
@@ -341,11 +341,24 @@ int long_clusters() {
   return n;
 }
 
+// The most keys that a tile of sixteen rows may read, by the lengths in use: a cache's capacity
+// says little about them (64 sequences of 1028 keys and 8 key heads in a cache of 131072 without
+// a window take 31 us unsplit and 104 split as that capacity would be).
+int64_t most_keys(const WindowArgs& a, const RowSpans& spans, int B) {
+  int64_t most = 0;
+  for (int b = 0; b < B; ++b) {
+    const KeyRange first = key_range(a, spans.start[b], spans.len[b]);
+    const KeyRange last = key_range(a, spans.start[b] + a.n_q - 1, spans.len[b]);
+    const int lo = min(first.lo, last.hi), keys = min(last.s, lo) + last.hi - lo;
+    if (keys > most) most = keys;
+  }
+  const int64_t window = (int64_t)a.left + a.right + 16 + a.sinks;
+  return window < most ? window : most;
+}
+
 cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, int sms, cudaStream_t st) {
   const int rows = a.n_q * (a.heads / a.kv_heads);
-  // the most keys a tile may read
-  const int64_t most = (int64_t)a.left + a.right + 16 + a.sinks;
-  const int64_t keys = most < a.n_kv ? most : a.n_kv;
+  const int64_t keys = most_keys(a, spans, B);
   // A tile is shared by as many CTAs as have a step for each of four warps, as long as all
   // CTAs run at once (three to an SM) or each warp has 16 steps to make up for their start and
   // join.  1028 keys, us for 8 / 4 / 2 / 1 CTAs: 32 tiles 6.4 / 7.1 / 9.6 / 14, 96 tiles 14.8 /
