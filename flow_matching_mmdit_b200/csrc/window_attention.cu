@@ -44,36 +44,7 @@ __host__ __device__ __forceinline__ KeyRange key_range(const WindowArgs& a, int 
   return r;
 }
 
-// One query row by one warp, reading attended keys only: lane l holds columns 2l and
-// 2l + 1, a key's score is a warp sum, and the softmax runs one key at a time.
-__device__ __forceinline__ void attend_row(const WindowArgs& a, int b, int h, int i, int p, int len) {
-  const int lane = threadIdx.x & 31;
-  const int64_t kv = ((int64_t)b * a.kv_heads + h / (a.heads / a.kv_heads)) * a.n_kv;
-  const uint32_t* q32 = reinterpret_cast<const uint32_t*>(a.q + (((int64_t)b * a.heads + h) * a.n_q + i) * 64);
-  const uint32_t* k32 = reinterpret_cast<const uint32_t*>(a.k + kv * 64);
-  const uint32_t* v32 = reinterpret_cast<const uint32_t*>(a.v + kv * 64);
-  const uint32_t qu = q32[lane];
-  const float q0 = bf16lo(qu), q1 = bf16hi(qu);
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-  const KeyRange r = key_range(a, p, len);
-  for (int j = r.s > 0 ? 0 : r.lo; j < r.hi; j = (j + 1 == r.s) ? max(r.lo, r.s) : j + 1) {
-    const uint32_t ku = k32[(int64_t)j * 32 + lane], vu = v32[(int64_t)j * 32 + lane];
-    float s = q0 * bf16lo(ku) + q1 * bf16hi(ku);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-    const float c = exp2f(m - base), e = exp2f(s - base);
-    m = mn;
-    l = l * c + e;
-    o0 = o0 * c + e * bf16lo(vu);
-    o1 = o1 * c + e * bf16hi(vu);
-  }
-  // a row with no attended key (or only scores of -inf) writes zeros
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  reinterpret_cast<uint32_t*>(a.out + (((int64_t)b * a.n_q + i) * a.heads + h) * 64)[lane] =
-      l == 0.f ? 0u : pack_bf16x2(o0 * inv, o1 * inv);
-}
+__device__ __forceinline__ bool attends(const KeyRange& r, int j) { return j < r.hi && (j >= r.lo || j < r.s); }
 
 // ------------------------------------------------------------------ few rows
 // The rows of one key head (its n_q queries times the heads that share it) in tiles of
@@ -99,33 +70,21 @@ __device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "f"(v) : "memory");
 }
 
-template <int SPLITS, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
-    window_attention_few_kernel(const __grid_constant__ WindowArgs a, const __grid_constant__ RowSpans spans) {
-  constexpr int splits = SPLITS, share = 16 / splits;     // rows that a CTA finishes
-  __shared__ float s_o[WARPS][16][66];                // O, maximum and sum of each warp
-  __shared__ float s_m[WARPS][16], s_l[WARPS][16];
-  __shared__ float s_part[splits][share][66];             // of each CTA: O, then maximum and sum
-  __shared__ int s_redo[16];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int rank = blockIdx.x % splits, tile = blockIdx.x / splits, hk = blockIdx.y, b = blockIdx.z;
-  const int group = a.heads / a.kv_heads, rows = a.n_q * group, row0 = tile * 16;
-  const int start = spans.start[b], len = spans.len[b];
-  // query of a row, exact since rows (48 queries of 1024 heads at most) times group stay below
-  // 2^32, and the head in its group
-  auto query = [&](int row) { return a.per_group ? (int)__umulhi(row, a.per_group) : row; };
-  auto member = [&](int row) { return row - query(row) * group; };
-  if constexpr (splits > 1) cluster_arrive();             // waited for before the others are written to
-  grid_dependency_sync();
-
-  // this thread's rows g and g + 8 (a row past the last repeats it and is not stored)
-  const int r_lo = min(row0 + g, rows - 1), r_hi = min(row0 + g + 8, rows - 1);
-  const KeyRange k_lo = key_range(a, start + query(r_lo), len), k_hi = key_range(a, start + query(r_hi), len);
+// The state of a warp's sixteen rows: thread (g, c) of lane 4 g + c holds rows g and g + 8, of
+// each the running maximum, its keys' share of the sum, and columns 16 c + j (o[j][0], o[j][2])
+// and 16 c + 8 + j (o[j][1], o[j][3]).
+struct Rows16 {
   uint32_t q[4][4];
-  {
-    const __nv_bfloat16* base = a.q + ((int64_t)b * a.heads + (int64_t)hk * group) * a.n_q * 64;
-    const __nv_bfloat16* p0 = base + ((int64_t)member(r_lo) * a.n_q + query(r_lo)) * 64 + 8 * c;
-    const __nv_bfloat16* p1 = base + ((int64_t)member(r_hi) * a.n_q + query(r_hi)) * 64 + 8 * c;
+  KeyRange k_lo, k_hi;                                  // of rows g and g + 8
+  float m0, m1, l0, l1, o[8][4];
+  __device__ __forceinline__ void clear() {
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  }
+  // p0 and p1: rows g and g + 8 from column 8 c on
+  __device__ __forceinline__ void load_q(const __nv_bfloat16* p0, const __nv_bfloat16* p1) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint4 x = *reinterpret_cast<const uint4*>(p0 + 32 * u), y = *reinterpret_cast<const uint4*>(p1 + 32 * u);
@@ -133,30 +92,61 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
       q[2 * u + 1][0] = x.z, q[2 * u + 1][1] = y.z, q[2 * u + 1][2] = x.w, q[2 * u + 1][3] = y.w;
     }
   }
-  // the keys any row of the tile attends: [0, sink) and [lo, hi), counted on through both
-  const KeyRange first = key_range(a, start + query(row0), len);
-  const KeyRange last = key_range(a, start + query(min(row0 + 15, rows - 1)), len);
-  const int hi = last.hi, lo = min(first.lo, hi), sink = min(last.s, lo);
-  const int count = sink + hi - lo;
-  const uint4 *kp = reinterpret_cast<const uint4*>(a.k + ((int64_t)b * a.kv_heads + hk) * a.n_kv * 64),
-              *vp = reinterpret_cast<const uint4*>(a.v + ((int64_t)b * a.kv_heads + hk) * a.n_kv * 64);
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, o[8][4] = {};
-  for (int at = (rank * WARPS + warp) * kFewStep; at < count; at += splits * WARPS * kFewStep) {
+  // each row's sum over the four threads that hold its keys
+  __device__ __forceinline__ void join_sums() {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  }
+};
+
+// The keys any of the rows attends, [0, sink) and [lo, hi), counted on through both.
+struct KeyUnion {
+  int sink, lo, count;
+  __device__ __forceinline__ KeyUnion(const KeyRange& first, const KeyRange& last) {
+    lo = min(first.lo, last.hi);
+    sink = min(last.s, lo);
+    count = sink + last.hi - lo;
+  }
+  __device__ __forceinline__ int key(int i) const { return i < sink ? i : lo + (i - sink); }
+};
+
+// Whether one of the two bf16 values is an infinity or NaN; and those values replaced by zero.
+__device__ __forceinline__ bool bf16x2_special(uint32_t v) {
+  return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t bf16x2_finite(uint32_t v) {
+  return ((v & 0x7f80u) == 0x7f80u ? 0u : v & 0xffffu) | ((v & 0x7f800000u) == 0x7f800000u ? 0u : v & 0xffff0000u);
+}
+
+// Steps of kFewStep keys, from `at` on every `stride` keys of the union.  A non-finite value in V
+// reaches every row of the tile through a weight of zero: with SAFE the values that go to the
+// tensor cores are finite, and each other one is added to the rows that attend its key.
+template <bool SAFE>
+__device__ __forceinline__ void attend_steps(Rows16& r, const KeyUnion& keys, const uint4* kp, const uint4* vp,
+                                             float scale_log2, int at, int stride) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (; at < keys.count; at += stride) {
     uint4 kr[4][2], vr[2][4];
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto load_v = [&] {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = at + 16 * t + 2 * c + (e & 1) + 4 * (e & 2);
+          vr[t][e] = i < keys.count ? vp[(int64_t)keys.key(i) * 8 + g] : zero;
+        }
+    };
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int i = at + 8 * t + g, j = i < sink ? i : lo + (i - sink);
+      const int i = at + 8 * t + g, j = keys.key(i);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) kr[t][u] = i < count ? kp[(int64_t)j * 8 + c + 4 * u] : zero;
+      for (int u = 0; u < 2; ++u) kr[t][u] = i < keys.count ? kp[(int64_t)j * 8 + c + 4 * u] : zero;
     }
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = at + 16 * t + 2 * c + (e & 1) + 4 * (e & 2), j = i < sink ? i : lo + (i - sink);
-        vr[t][e] = i < count ? vp[(int64_t)j * 8 + g] : zero;
-      }
+    if constexpr (!SAFE) load_v();
     float s[4][4];
     float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
@@ -165,37 +155,36 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
       for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        mma_bf16(s[t], q[2 * u], kr[t][u].x, kr[t][u].y);
-        mma_bf16(s[t], q[2 * u + 1], kr[t][u].z, kr[t][u].w);
+        mma_bf16(s[t], r.q[2 * u], kr[t][u].x, kr[t][u].y);
+        mma_bf16(s[t], r.q[2 * u + 1], kr[t][u].z, kr[t][u].w);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int i = at + 8 * t + 2 * c + e, j = i < sink ? i : lo + (i - sink);
-        const bool in = i < count;
-        const bool on0 = in && j < k_lo.hi && (j >= k_lo.lo || j < k_lo.s);
-        const bool on1 = in && j < k_hi.hi && (j >= k_hi.lo || j < k_hi.s);
-        s[t][e] = on0 ? s[t][e] * a.scale_log2 : -INFINITY;
-        s[t][2 + e] = on1 ? s[t][2 + e] * a.scale_log2 : -INFINITY;
+        const int i = at + 8 * t + 2 * c + e, j = keys.key(i);
+        const bool in = i < keys.count;
+        s[t][e] = in && attends(r.k_lo, j) ? s[t][e] * scale_log2 : -INFINITY;
+        s[t][2 + e] = in && attends(r.k_hi, j) ? s[t][2 + e] * scale_log2 : -INFINITY;
         x0 = fmaxf(x0, s[t][e]);
         x1 = fmaxf(x1, s[t][2 + e]);
       }
     }
+    if constexpr (SAFE) load_v();                        // in the place of K, which is done with
     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-    x0 = fmaxf(m0, fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2)));
-    x1 = fmaxf(m1, fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2)));
+    x0 = fmaxf(r.m0, fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2)));
+    x1 = fmaxf(r.m1, fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2)));
     const float b0 = x0 == -INFINITY ? 0.f : x0, b1 = x1 == -INFINITY ? 0.f : x1;
-    const float c0 = ex2(m0 - b0), c1 = ex2(m1 - b1);
-    m0 = x0;
-    m1 = x1;
-    l0 *= c0;
-    l1 *= c1;
+    const float c0 = ex2(r.m0 - b0), c1 = ex2(r.m1 - b1);
+    r.m0 = x0;
+    r.m1 = x1;
+    r.l0 *= c0;
+    r.l1 *= c1;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      o[j][0] *= c0;
-      o[j][1] *= c0;
-      o[j][2] *= c1;
-      o[j][3] *= c1;
+      r.o[j][0] *= c0;
+      r.o[j][1] *= c0;
+      r.o[j][2] *= c1;
+      r.o[j][3] *= c1;
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -203,9 +192,48 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
       for (int e = 0; e < 2; ++e) {
         s[t][e] = ex2(s[t][e] - b0);
         s[t][2 + e] = ex2(s[t][2 + e] - b1);
-        l0 += s[t][e];
-        l1 += s[t][2 + e];
+        r.l0 += s[t][e];
+        r.l1 += s[t][2 + e];
       }
+    if constexpr (SAFE) {
+      uint32_t special = 0;                              // keys of this step with such values
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4& v = vr[t][e];
+          if (bf16x2_special(v.x) || bf16x2_special(v.y) || bf16x2_special(v.z) || bf16x2_special(v.w)) {
+            special |= 1u << (16 * t + 2 * c + (e & 1) + 4 * (e & 2));
+            v = make_uint4(bf16x2_finite(v.x), bf16x2_finite(v.y), bf16x2_finite(v.z), bf16x2_finite(v.w));
+          }
+        }
+      special = __reduce_or_sync(0xffffffffu, special);
+      for (; special; special &= special - 1) {
+        const int i = __ffs(special) - 1, j = keys.key(at + i);
+        float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (t == i >> 3 && e == (i & 1)) w0 = s[t][e], w1 = s[t][2 + e];
+        w0 = __shfl_sync(0xffffffffu, w0, (lane & ~3) | ((i >> 1) & 3));
+        w1 = __shfl_sync(0xffffffffu, w1, (lane & ~3) | ((i >> 1) & 3));
+        const bool on0 = attends(r.k_lo, j), on1 = attends(r.k_hi, j);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint4 v4 = vp[(int64_t)j * 8 + 2 * c + u];
+          const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const float x = n & 1 ? bf16hi(v[n >> 1]) : bf16lo(v[n >> 1]);
+            if (!isfinite(x)) {
+              if (on0) r.o[n][u] += w0 * x;
+              if (on1) r.o[n][2 + u] += w1 * x;
+            }
+          }
+        }
+      }
+    }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       // the weights are rounded to bf16 for the tensor cores; their sum is not
@@ -221,27 +249,71 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-        mma_bf16(o[j], p, __byte_perm(w[0][j >> 1], w[1][j >> 1], sel), __byte_perm(w[2][j >> 1], w[3][j >> 1], sel));
+        mma_bf16(r.o[j], p, __byte_perm(w[0][j >> 1], w[1][j >> 1], sel),
+                 __byte_perm(w[2][j >> 1], w[3][j >> 1], sel));
       }
     }
   }
+}
+
+template <int SPLITS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
+    window_attention_few_kernel(const __grid_constant__ WindowArgs a, const __grid_constant__ RowSpans spans) {
+  constexpr int splits = SPLITS, share = 16 / splits;     // rows that a CTA finishes
+  __shared__ float s_o[WARPS][16][66];                // O, maximum and sum of each warp
+  __shared__ float s_m[WARPS][16], s_l[WARPS][16];
+  __shared__ float s_part[splits][share][66];             // of each CTA: O, then maximum and sum
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int rank = blockIdx.x % splits, tile = blockIdx.x / splits, hk = blockIdx.y, b = blockIdx.z;
+  const int group = a.heads / a.kv_heads, rows = a.n_q * group, row0 = tile * 16;
+  const int start = spans.start[b], len = spans.len[b];
+  // query of a row, exact since rows (48 queries of 1024 heads at most) times group stay below
+  // 2^32, and the head in its group
+  auto query = [&](int row) { return a.per_group ? (int)__umulhi(row, a.per_group) : row; };
+  auto member = [&](int row) { return row - query(row) * group; };
+  if constexpr (splits > 1) cluster_arrive();             // waited for before the others are written to
+  grid_dependency_sync();
+
+  // this thread's rows g and g + 8 (a row past the last repeats it and is not stored)
+  const int r_lo = min(row0 + g, rows - 1), r_hi = min(row0 + g + 8, rows - 1);
+  Rows16 t;
+  t.k_lo = key_range(a, start + query(r_lo), len);
+  t.k_hi = key_range(a, start + query(r_hi), len);
+  const __nv_bfloat16* q = a.q + ((int64_t)b * a.heads + (int64_t)hk * group) * a.n_q * 64 + 8 * c;
+  t.load_q(q + ((int64_t)member(r_lo) * a.n_q + query(r_lo)) * 64,
+           q + ((int64_t)member(r_hi) * a.n_q + query(r_hi)) * 64);
+  const KeyUnion keys(key_range(a, start + query(row0), len),
+                      key_range(a, start + query(min(row0 + 15, rows - 1)), len));
+  const uint4 *kp = reinterpret_cast<const uint4*>(a.k + ((int64_t)b * a.kv_heads + hk) * a.n_kv * 64),
+              *vp = reinterpret_cast<const uint4*>(a.v + ((int64_t)b * a.kv_heads + hk) * a.n_kv * 64);
+  const int at = (rank * WARPS + warp) * kFewStep, stride = splits * WARPS * kFewStep;
+  t.clear();
+  attend_steps<false>(t, keys, kp, vp, a.scale_log2, at, stride);
+  t.join_sums();
+  // A part that came out non-finite is done again, unless a score is NaN and so the whole row.
+  float bad0 = 0.f, bad1 = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    bad0 += (t.o[j][0] + t.o[j][1]) * 0.f;
+    bad1 += (t.o[j][2] + t.o[j][3]) * 0.f;
+  }
+  if (__any_sync(0xffffffffu, (isnan(bad0) && !isnan(t.l0)) || (isnan(bad1) && !isnan(t.l1)))) {
+    t.clear();
+    attend_steps<true>(t, keys, kp, vp, a.scale_log2, at, stride);
+    t.join_sums();
+  }
   // ---- join the warps, then the CTAs
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
   if (c == 0) {
-    s_m[warp][g] = m0, s_m[warp][g + 8] = m1;
-    s_l[warp][g] = l0, s_l[warp][g + 8] = l1;
+    s_m[warp][g] = t.m0, s_m[warp][g + 8] = t.m1;
+    s_l[warp][g] = t.l0, s_l[warp][g + 8] = t.l1;
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    s_o[warp][g][16 * c + j] = o[j][0];
-    s_o[warp][g][16 * c + 8 + j] = o[j][1];
-    s_o[warp][g + 8][16 * c + j] = o[j][2];
-    s_o[warp][g + 8][16 * c + 8 + j] = o[j][3];
+    s_o[warp][g][16 * c + j] = t.o[j][0];
+    s_o[warp][g][16 * c + 8 + j] = t.o[j][1];
+    s_o[warp][g + 8][16 * c + j] = t.o[j][2];
+    s_o[warp][g + 8][16 * c + 8 + j] = t.o[j][3];
   }
-  if (threadIdx.x < 16) s_redo[threadIdx.x] = 0;
   __syncthreads();
   if constexpr (splits > 1) cluster_wait();
   for (int e = threadIdx.x; e < 16 * 64; e += 32 * WARPS) {
@@ -302,15 +374,8 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
     if (row0 + r < rows) {
       const int i = query(row0 + r), h = hk * group + member(row0 + r);
       a.out[(((int64_t)b * a.n_q + i) * a.heads + h) * 64 + d] = __float2bfloat16_rn(y);
-      if (!isfinite(y)) s_redo[r] = 1;
     }
   }
-  __syncthreads();
-  // A non-finite value in V reaches the whole tile through a weight of zero: rows that came
-  // out non-finite are done again from their attended keys alone.
-  for (int r = rank * share + warp; r < (rank + 1) * share; r += WARPS)
-    if (s_redo[r])
-      attend_row(a, b, hk * group + member(row0 + r), query(row0 + r), start + query(row0 + r), len);
 }
 
 // Clusters of kFewLongSplit CTAs that the current device runs at a time (0: none), looked up once
@@ -397,6 +462,39 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, int sm
     case 2: return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<2, 4>, a, spans);
     case 4: return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<4, 4>, a, spans);
     default: return cudaLaunchKernelEx(&cfg, window_attention_few_kernel<8, 4>, a, spans);
+  }
+}
+
+// The rows `redo` of the sixteen from t0 on of one head, from their keys alone, by one warp.  (A
+// call, so that the many-row kernel's own registers are not spilled for it: 1 % there.)  With an
+// infinity that every row attends, 8356 tokens, window 1024 + 1024, 256 sinks and 24 heads take
+// 1.9 ms for 0.19; one row and one key at a time took 61.
+__device__ __noinline__ void redo_rows(const WindowArgs& a, int b, int h, int bhk, int t0, int start, int len,
+                                       uint32_t redo) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, last = min(t0 + 15, a.n_q - 1);
+  Rows16 t;
+  t.k_lo = key_range(a, start + t0 + g, len);
+  t.k_hi = key_range(a, start + t0 + g + 8, len);
+  const __nv_bfloat16* q = a.q + ((int64_t)b * a.heads + h) * a.n_q * 64 + 8 * c;
+  t.load_q(q + (int64_t)min(t0 + g, last) * 64, q + (int64_t)min(t0 + g + 8, last) * 64);
+  t.clear();
+  attend_steps<true>(t, KeyUnion(key_range(a, start + t0, len), key_range(a, start + last, len)),
+                     reinterpret_cast<const uint4*>(a.k + (int64_t)bhk * a.n_kv * 64),
+                     reinterpret_cast<const uint4*>(a.v + (int64_t)bhk * a.n_kv * 64), a.scale_log2, 0, kFewStep);
+  t.join_sums();
+#pragma unroll
+  for (int rr = 0; rr < 2; ++rr) {
+    const float lr = rr ? t.l1 : t.l0, inv = lr > 0.f ? 1.f / lr : 0.f;
+    const int row = g + 8 * rr;
+    if (!((redo >> row) & 1)) continue;
+    uint4* to = reinterpret_cast<uint4*>(a.out + (((int64_t)b * a.n_q + t0 + row) * a.heads + h) * 64) + 2 * c;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(t.o[2 * j][2 * rr + u] * inv, t.o[2 * j + 1][2 * rr + u] * inv);
+      to[u] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -856,14 +954,15 @@ __global__ void __launch_bounds__(THREADS, 2)
         // a row with no attended key (l = 0) writes zeros rather than 0 * inf
         const float lr = rr ? l1 : l0;
         const float inv = lr > 0.f ? 1.f / lr : 0.f;
-        float bad = lr * 0.f;                              // 0, or NaN
+        float bad = 0.f;                                   // 0, or NaN
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           bad += (o[4 * g + 2 * rr] + o[4 * g + 2 * rr + 1]) * 0.f;
           *reinterpret_cast<uint32_t*>(stage + r * 128 + ((g ^ (r & 7)) << 4) + 2 * cq) =
               lr == 0.f ? 0u : pack_bf16x2(o[4 * g + 2 * rr] * inv, o[4 * g + 2 * rr + 1] * inv);
         }
-        uint32_t v = __ballot_sync(0xffffffffu, bad != 0.f && q0 + wrow + r < a.n_q);
+        // (with a NaN among the scores the whole row is NaN, as it should be)
+        uint32_t v = __ballot_sync(0xffffffffu, bad != 0.f && lr > 0.f && q0 + wrow + r < a.n_q);
         v |= v >> 1;
         v |= v >> 2;                                       // bit 4 r: row r's four threads
 #pragma unroll
@@ -878,12 +977,9 @@ __global__ void __launch_bounds__(THREADS, 2)
               *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
       }
       // A non-finite value in V reaches the whole tile through a weight of zero: such rows
-      // are done again from their attended keys alone.
+      // are done again, the warp's sixteen together.
       __syncwarp();
-      for (; redo; redo &= redo - 1) {
-        const int i = q0 + wrow + __ffs(redo) - 1;
-        attend_row(a, b, h, i, start + i, len);
-      }
+      if (redo) redo_rows(a, b, h, bhk, q0 + wrow, start, len, redo);
     }
   }
   tc_fence_before();

@@ -434,8 +434,9 @@ LENS_API lens_status lens_op_sandwich_norm(const float* h, const void* y, lens_d
  *   q_start  host int [B], >= 0, or NULL (0);  kv_len host int [B], 0..n_kv, or NULL (n_kv)
  *   left, right  >= 0, or -1 for no bound on that side;  sinks >= 0
  * Keys that a query does not attend have no effect on its output, whatever K and V hold
- * there (rows near a non-finite value in V take longer and round differently).  n_q may be anything from one
- * token against a long cache to all of them.  (For few queries, up to about 48, the keys are
+ * there.  Rows of a tile that reads an infinity or NaN in V are computed a second time, which may
+ * round differently; where every row attends one, a call takes up to ten times as long.  n_q may be
+ * anything from one token against a long cache to all of them.  (For few queries, up to about 48, the keys are
  * split over more CTAs in a small batch than in a large one, so the last bit of a row may
  * depend on the batch; for more queries it does not.)  B <= 64; heads a multiple of kv_heads, at
  * most 1024; q, k, v, out 16-byte aligned; out must not overlap q, k or v.
