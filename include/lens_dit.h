@@ -390,7 +390,10 @@ LENS_API lens_status lens_op_quantize_f8(const void* x, lens_dtype x_type, int64
  * w_scales [ceil(K/128), ceil(N/128)] (block_rows 128),
  *   C[m, n] = sum_g a_scales[g][m] w_scales[g][n / 128] sum_{k in g} A[m, k] W[n, k] (+ bias[n])
  * on the 8-bit tensor cores, each 128-wide block accumulated in fp32, scaled and added
- * in fp32.
+ * in fp32.  The two scales of a block are multiplied first, in fp32: their product has to
+ * be 0 or from 2^-126 to below 2^128.  (Below, the block's share loses bits or is lost; above, it is
+ * infinite, and NaN where the block sums to 0.  Scales of lens_op_quantize_f8 are inside as long as
+ * the largest magnitudes of the two blocks multiply to 2^-108 .. 2^145, or one block is all zeros.)
  *   A dev e4m3 [M, K], W dev e4m3 [N, K], bias dev fp32 [N] or NULL,
  *   C dev [M, N], fp32 or bf16 (c_type, rounded once).  A, W, C 16-byte aligned, C overlapping
  *   none of the inputs.
