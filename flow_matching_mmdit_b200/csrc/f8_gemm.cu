@@ -5,6 +5,7 @@
 
 #include "f32x2.cuh"
 #include "f8.cuh"
+#include "f8_gemm_choice.h"
 #include "gemm.h"
 #include "gemm_tc.cuh"
 #include "kernels.cuh"
@@ -755,36 +756,17 @@ cudaError_t launch_few(const F8Gemm& g, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_gemm_f8(const F8Gemm& g, int* err, int sms, cudaStream_t st) {
-  const int64_t kblocks = (g.K + kF8Group - 1) / kF8Group, weights = (int64_t)g.N * g.K;
-  // Up to 32 rows, few weights and no long k.  us, mma.sync for 128-row tiles of W by tcgen05:
-  // 8 rows, 4608 x 1536 3.4 for 4.6, 4096 x 8192 11.0 for 8.7; 16 rows, 1536 x 4096 4.0 for 4.4,
-  // 8192 x 1536 7.5 for 5.3, 128 x 11520 6.9 for 5.6; 32 rows, 2304 x 1536 3.9 for 4.1,
-  // 1536 x 4096 6.5 for 4.6.
-  const int groups = g.M <= 8 ? 1 : g.M <= 16 ? 2 : 4;
-  if (g.M <= 32 && groups * weights <= 1 << 24 && groups * kblocks <= 96)
-    return groups == 1 ? launch_few<1>(g, st) : groups == 2 ? launch_few<2>(g, st) : launch_few<4>(g, st);
-  // 128 x 128 tiles, each with as many CTAs as there are k blocks for while all clusters find
-  // room at once (of 36 clusters of four CTAs one waits: 4608 x 1536, 64 rows 8.9 us for 5.6 with
-  // two): where there is one row of tiles or room for two CTAs a tile.  us, for CTA pairs: 64
-  // rows, 1536 x 4096 5.3 for 8.4, 4096 x 8192 9.9 for 21.5, 24576 x 1536 16.7 for 18.4; 77 rows,
-  // 1536 x 4096 6.1 for 8.5, 16384 x 2048 12.6 for 14.7, 24576 x 1536 (more tiles than SMs) 19.8
-  // for 17.4; 200 rows, 1536 x 1536 6.4 for 7.6, 1536 x 4096 8.4 for 12.9, 4608 x 1536 (no room
-  // for two) 9.4 for 8.0; 640 rows, 768 x 4096 8.7 for 13.1, 1536 x 1536 8.0 for 8.0.
-  const int64_t tiles = (g.N + kF8Group - 1) / kF8Group * (g.M <= 64 ? 1 : (g.M + 127) / 128);
-  int l2 = 0;
-  while (l2 < 3 && kblocks >= 2 << l2 && 8 * (2 * tiles << l2) <= 7 * sms) ++l2;
-  if (g.M <= 64) return g.bf16 ? launch_mid<32, true>(g, l2, err, st) : launch_mid<32, false>(g, l2, err, st);
-  if (l2 > 0 || (g.M <= 128 && tiles <= sms))
-    return g.bf16 ? launch_mid<64, true>(g, l2, err, st) : launch_mid<64, false>(g, l2, err, st);
-  const int64_t tiles_m = (g.M + 255) / 256, pairs = sms / 2;
-  const int64_t narrow_tiles = tiles_m * ((g.N + 127) / 128), wide_tiles = tiles_m * ((g.N + 255) / 256);
-  // 256-wide tiles load and wait less a column, but only where their rounds on the pairs
-  // come near half of the 128-wide ones': sustained, us, 8704 x 8192 x 1536 (15 rounds for 30)
-  // 135 for 142, 8704 x 1536 x 4096 (3 for 6) 65 for 72, 4352 x 4608 x 1536 (5 for 9) 43 for
-  // 44, 4352 x 1536 x 4096 (2 for 3) 39 for 37, 1152 x 8192 x 1536 (3 for 5) 26 for 23
-  const int64_t wide = (wide_tiles + pairs - 1) / pairs, narrow = (narrow_tiles + pairs - 1) / pairs;
-  if (7 * wide <= 4 * narrow) return launch_pair<2>(g, err, sms, st);
-  return launch_pair<1>(g, err, sms, st);
+  const F8Choice c = choose_gemm_f8(g.M, g.N, g.K, sms);
+  switch (c.kernel) {
+    case kF8Few:
+      return c.detail == 1 ? launch_few<1>(g, st) : c.detail == 2 ? launch_few<2>(g, st) : launch_few<4>(g, st);
+    case kF8Mid64:
+      return g.bf16 ? launch_mid<32, true>(g, c.detail, err, st) : launch_mid<32, false>(g, c.detail, err, st);
+    case kF8Mid128:
+      return g.bf16 ? launch_mid<64, true>(g, c.detail, err, st) : launch_mid<64, false>(g, c.detail, err, st);
+    case kF8Pair256: return launch_pair<2>(g, err, sms, st);
+    default: return launch_pair<1>(g, err, sms, st);
+  }
 }
 
 }  // namespace lens

@@ -30,6 +30,31 @@ def test_a_row_does_not_depend_on_the_capacity_of_the_cache(n_q):
     assert torch.equal(run(q, big[0], big[1], start, length, -1, 0, 0), want)
 
 
+@pytest.mark.parametrize("sinks", [16, 17, 40, 100, 127, 128, 129])
+@pytest.mark.parametrize("B,H,Hk,n_q,n_kv,left,right", [(1, 2, 1, 600, 600, 60, 0), (2, 3, 3, 300, 700, 130, 40),
+                                                        (1, 4, 2, 20, 900, 100, 0), (1, 2, 2, 260, 260, 0, 0)])
+def test_sinks_around_a_key_tile(B, H, Hk, n_q, n_kv, left, right, sinks):
+    """Up to 16 sinks are a tile of their own size, more of them a masked tile of 128, or two."""
+    q, k, v = make(B, H, Hk, n_q, n_kv, sinks)
+    length = [n_kv - 37 * b for b in range(B)]
+    start = [n - n_q for n in length]
+    check(run(q, k, v, start, length, left, right, sinks), q, k, v, start, length, left, right, sinks)
+
+
+@pytest.mark.parametrize("n_q,n_kv", [(1, 2000), (40, 900), (300, 300)])
+def test_the_same_bits_from_a_side_stream_and_beside_other_work(n_q, n_kv):
+    q, k, v = make(2, 6, 2, n_q, n_kv, 14)
+    start = [n_kv - n_q, n_kv - n_q]
+    want = run(q, k, v, start, None, 70, 0, 4).clone()
+    outs = [torch.full_like(want, -7.0) for _ in range(6)]
+    torch.cuda.synchronize()                        # the fills come before the streams' work
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for i, o in enumerate(outs):
+        L.lens_op_attention_window(q, k, v, 2, 6, 2, n_q, n_kv, start, None, 70, 0, 4, 0.125, o, stream=streams[i % 3])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 def expected(q, k, v, start, length, left, right, sinks, b, h):
     """(fp64 output, sum p |v|) of one head with every non-finite value of V taken as 0, and the
     output's infinities and NaNs: what the attended values of a column sum to, where it is not
