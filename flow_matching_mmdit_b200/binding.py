@@ -449,14 +449,14 @@ def _rows(where: str, dev: int, x, samples: int = 1, D: int = 0, mod_stride: int
     dimension of its own, or anywhere in a contiguous tensor that is long enough) is refused."""
     if x is None:
         return None
-    if x.get_device() != dev or x.stride(-1) != 1:
+    shape, stride = x.shape, x.stride()          # as tuples: one entry of a method's costs as much as all
+    if x.get_device() != dev or stride[-1] != 1:
         raise LensError(1, where)
-    if x.size(-1) >= D:
-        if samples <= 1 or mod_stride == 0:
+    if shape[-1] >= D:
+        if samples <= 1 or mod_stride == 0 or (stride[0] == mod_stride and shape[0] >= samples):
             return x.data_ptr()
-        for i in range(x.dim() - 1):
-            if x.stride(i) == mod_stride and x.size(i) >= samples:
-                return x.data_ptr()
+        if any(t == mod_stride and n >= samples for t, n in zip(stride[1:-1], shape[1:])):
+            return x.data_ptr()
     if not x.is_contiguous() or x.numel() < (samples - 1) * mod_stride + D:
         raise LensError(2, where)
     return x.data_ptr()
