@@ -35,10 +35,12 @@ namespace {
 //   tfull[j]   (both)    slot j holds a k block's P_g, and its scales have landed
 //   tempty[j]  (leader)  both CTAs' epilogue warps have read slot j
 //   sfree[j]   (each)    this CTA's epilogue warps have read slot j's scales
-// Per k block and pair of a 256 x 128 tile about 330 ns pass at 8704 x 8192 x 1536: the MMAs
-// alone would take 150 and L2 delivers a pair's 48 KB in 230 (10 TB/s, as for the bf16
-// products); the rest is the way through a slot (MMA, commit, read, release, next MMA), of
-// which four run at a time, or two of twice the width.
+// A k block takes a pair 260 to 290 ns in a 256 x 128 tile (1021 x 2000) and 490 to 530 in a
+// 256 x 256 one (8704 x 8192), its four MMAs alone about 150 and 300; a tile's start and output
+// add about 5 us.  Of the wide tile's 1050 clocks a block, 512 are the MMAs, 800 pass with MMAs and
+// loads but no adding (what makes up the difference is open: L2 runs at 29 % of its throughput), and
+// the rest is the way through a slot (MMA, commit, read, release, next MMA), of which two run at a
+// time, or four of half the width.
 template <int HALVES>
 struct F8Cfg {
   static constexpr int BN = 128 * HALVES, COLS = BN / 2;   // COLS: columns a thread accumulates

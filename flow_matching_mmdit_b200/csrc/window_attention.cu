@@ -112,146 +112,176 @@ struct KeyUnion {
   __device__ __forceinline__ int key(int i) const { return i < sink ? i : lo + (i - sink); }
 };
 
-// Whether one of the two bf16 values is an infinity or NaN; and those values replaced by zero.
+// Infinities and NaNs of two bf16 values: whether there is one; the values without them; and each
+// as a number of its own, 1 for +inf, 64 for -inf and 4096 for NaN (0 for a finite value), so that
+// a sum of 32 of them says which it holds.
 __device__ __forceinline__ bool bf16x2_special(uint32_t v) {
   return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
 }
 __device__ __forceinline__ uint32_t bf16x2_finite(uint32_t v) {
   return ((v & 0x7f80u) == 0x7f80u ? 0u : v & 0xffffu) | ((v & 0x7f800000u) == 0x7f800000u ? 0u : v & 0xffff0000u);
 }
+__device__ __forceinline__ uint32_t bf16x2_marks(uint32_t v) {
+  auto mark = [](uint32_t h) {
+    return (h & 0x7f80u) != 0x7f80u ? 0u : h & 0x7fu ? 0x4580u : h & 0x8000u ? 0x4280u : 0x3f80u;
+  };
+  return mark(v & 0xffffu) | (mark(v >> 16) << 16);
+}
+// What the marked values add up to: 0, an infinity or NaN.
+__device__ __forceinline__ float marked_sum(float marks) {
+  const int n = (int)marks;
+  const bool plus = n & 63, minus = n & (63 << 6);
+  const float inf = plus ? INFINITY : -INFINITY;
+  return n == 0 ? 0.f : n >= 4096 || (plus && minus) ? NAN : inf;
+}
 
-// Steps of kFewStep keys, from `at` on every `stride` keys of the union.  A non-finite value in V
-// reaches every row of the tile through a weight of zero: with SAFE the values that go to the
-// tensor cores are finite, and each other one is added to the rows that attend its key.
-template <bool SAFE>
-__device__ __forceinline__ void attend_steps(Rows16& r, const KeyUnion& keys, const uint4* kp, const uint4* vp,
-                                             float scale_log2, int at, int stride) {
+// GROUPS groups of eight keys of the union, from its key `at` on.  A non-finite value in V reaches
+// every row of the tile through a weight of zero: with SAFE the values that go to the tensor cores
+// are finite, and a second product, of which keys a row attends with where the others stand, adds
+// those to the rows that attend them.
+template <int GROUPS, bool SAFE>
+__device__ __forceinline__ void attend_step(Rows16& r, const KeyUnion& keys, const uint4* kp, const uint4* vp,
+                                            float scale_log2, int at) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-  for (; at < keys.count; at += stride) {
-    uint4 kr[4][2], vr[2][4];
-    auto load_v = [&] {
+  uint4 kr[GROUPS][2], vr[GROUPS / 2][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+  for (int t = 0; t < GROUPS; ++t) {
+    const int i = at + 8 * t + g, j = keys.key(i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = at + 16 * t + 2 * c + (e & 1) + 4 * (e & 2);
-          vr[t][e] = i < keys.count ? vp[(int64_t)keys.key(i) * 8 + g] : zero;
+    for (int u = 0; u < 2; ++u) kr[t][u] = i < keys.count ? kp[(int64_t)j * 8 + c + 4 * u] : zero;
+  }
+#pragma unroll
+  for (int t = 0; t < GROUPS / 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = at + 16 * t + 2 * c + (e & 1) + 4 * (e & 2);
+      vr[t][e] = i < keys.count ? vp[(int64_t)keys.key(i) * 8 + g] : zero;
+    }
+  float s[GROUPS][4];
+  float x0 = -INFINITY, x1 = -INFINITY;
+  uint32_t attended = 0;                                 // bit 4 t + e: s[t][e]
+#pragma unroll
+  for (int t = 0; t < GROUPS; ++t) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      mma_bf16(s[t], r.q[2 * u], kr[t][u].x, kr[t][u].y);
+      mma_bf16(s[t], r.q[2 * u + 1], kr[t][u].z, kr[t][u].w);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = at + 8 * t + 2 * c + e, j = keys.key(i);
+      const bool in = i < keys.count;
+      // (named, the two conditions are worked out ahead of the products and spill registers: 6.2 us for
+      // 5.4 with one query of 1028 keys)
+      s[t][e] = in && attends(r.k_lo, j) ? s[t][e] * scale_log2 : -INFINITY;
+      s[t][2 + e] = in && attends(r.k_hi, j) ? s[t][2 + e] * scale_log2 : -INFINITY;
+      if constexpr (SAFE) {
+        attended |= (uint32_t)(in && attends(r.k_lo, j)) << (4 * t + e);
+        attended |= (uint32_t)(in && attends(r.k_hi, j)) << (4 * t + 2 + e);
+      }
+      x0 = fmaxf(x0, s[t][e]);
+      x1 = fmaxf(x1, s[t][2 + e]);
+    }
+  }
+  x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+  x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+  x0 = fmaxf(r.m0, fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2)));
+  x1 = fmaxf(r.m1, fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2)));
+  const float b0 = x0 == -INFINITY ? 0.f : x0, b1 = x1 == -INFINITY ? 0.f : x1;
+  const float c0 = ex2(r.m0 - b0), c1 = ex2(r.m1 - b1);
+  r.m0 = x0;
+  r.m1 = x1;
+  r.l0 *= c0;
+  r.l1 *= c1;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    r.o[j][0] *= c0;
+    r.o[j][1] *= c0;
+    r.o[j][2] *= c1;
+    r.o[j][3] *= c1;
+  }
+#pragma unroll
+  for (int t = 0; t < GROUPS; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      s[t][e] = ex2(s[t][e] - b0);
+      s[t][2 + e] = ex2(s[t][2 + e] - b1);
+      r.l0 += s[t][e];
+      r.l1 += s[t][2 + e];
+    }
+  if constexpr (SAFE) {
+    bool special = false;
+#pragma unroll
+    for (int t = 0; t < GROUPS / 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        special = special || bf16x2_special(vr[t][e].x) || bf16x2_special(vr[t][e].y) ||
+                  bf16x2_special(vr[t][e].z) || bf16x2_special(vr[t][e].w);
+    if (__any_sync(0xffffffffu, special)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float marks[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+#pragma unroll
+        for (int t = 0; t < GROUPS / 2; ++t) {
+          uint32_t w[4], ones[4];                        // ones: 1 where the row attends the key
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4& v = vr[t][e];
+            w[e] = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
+            const uint32_t b = attended >> (8 * t + 2 * e);
+            ones[e] = (b & 1u ? 0x3f80u : 0u) | (b & 2u ? 0x3f800000u : 0u);
+          }
+          mma_bf16(marks, ones, bf16x2_marks(__byte_perm(w[0], w[1], sel)),
+                   bf16x2_marks(__byte_perm(w[2], w[3], sel)));
         }
-    };
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int i = at + 8 * t + g, j = keys.key(i);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) kr[t][u] = i < keys.count ? kp[(int64_t)j * 8 + c + 4 * u] : zero;
-    }
-    if constexpr (!SAFE) load_v();
-    float s[4][4];
-    float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        mma_bf16(s[t], r.q[2 * u], kr[t][u].x, kr[t][u].y);
-        mma_bf16(s[t], r.q[2 * u + 1], kr[t][u].z, kr[t][u].w);
+        for (int e = 0; e < 4; ++e) r.o[j][e] += marked_sum(marks[e]);
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = at + 8 * t + 2 * c + e, j = keys.key(i);
-        const bool in = i < keys.count;
-        s[t][e] = in && attends(r.k_lo, j) ? s[t][e] * scale_log2 : -INFINITY;
-        s[t][2 + e] = in && attends(r.k_hi, j) ? s[t][2 + e] * scale_log2 : -INFINITY;
-        x0 = fmaxf(x0, s[t][e]);
-        x1 = fmaxf(x1, s[t][2 + e]);
-      }
-    }
-    if constexpr (SAFE) load_v();                        // in the place of K, which is done with
-    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-    x0 = fmaxf(r.m0, fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2)));
-    x1 = fmaxf(r.m1, fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2)));
-    const float b0 = x0 == -INFINITY ? 0.f : x0, b1 = x1 == -INFINITY ? 0.f : x1;
-    const float c0 = ex2(r.m0 - b0), c1 = ex2(r.m1 - b1);
-    r.m0 = x0;
-    r.m1 = x1;
-    r.l0 *= c0;
-    r.l1 *= c1;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      r.o[j][0] *= c0;
-      r.o[j][1] *= c0;
-      r.o[j][2] *= c1;
-      r.o[j][3] *= c1;
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[t][e] = ex2(s[t][e] - b0);
-        s[t][2 + e] = ex2(s[t][2 + e] - b1);
-        r.l0 += s[t][e];
-        r.l1 += s[t][2 + e];
-      }
-    if constexpr (SAFE) {
-      uint32_t special = 0;                              // keys of this step with such values
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < GROUPS / 2; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint4& v = vr[t][e];
-          if (bf16x2_special(v.x) || bf16x2_special(v.y) || bf16x2_special(v.z) || bf16x2_special(v.w)) {
-            special |= 1u << (16 * t + 2 * c + (e & 1) + 4 * (e & 2));
-            v = make_uint4(bf16x2_finite(v.x), bf16x2_finite(v.y), bf16x2_finite(v.z), bf16x2_finite(v.w));
-          }
+          v = make_uint4(bf16x2_finite(v.x), bf16x2_finite(v.y), bf16x2_finite(v.z), bf16x2_finite(v.w));
         }
-      special = __reduce_or_sync(0xffffffffu, special);
-      for (; special; special &= special - 1) {
-        const int i = __ffs(special) - 1, j = keys.key(at + i);
-        float w0 = 0.f, w1 = 0.f;
+    }
+  }
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < GROUPS / 2; ++t) {
+    // the weights are rounded to bf16 for the tensor cores; their sum is not
+    const uint32_t p[4] = {pack_bf16x2(s[2 * t][0], s[2 * t][1]), pack_bf16x2(s[2 * t][2], s[2 * t][3]),
+                           pack_bf16x2(s[2 * t + 1][0], s[2 * t + 1][1]),
+                           pack_bf16x2(s[2 * t + 1][2], s[2 * t + 1][3])};
+    uint32_t w[4][4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (t == i >> 3 && e == (i & 1)) w0 = s[t][e], w1 = s[t][2 + e];
-        w0 = __shfl_sync(0xffffffffu, w0, (lane & ~3) | ((i >> 1) & 3));
-        w1 = __shfl_sync(0xffffffffu, w1, (lane & ~3) | ((i >> 1) & 3));
-        const bool on0 = attends(r.k_lo, j), on1 = attends(r.k_hi, j);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint4 v4 = vp[(int64_t)j * 8 + 2 * c + u];
-          const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const float x = n & 1 ? bf16hi(v[n >> 1]) : bf16lo(v[n >> 1]);
-            if (!isfinite(x)) {
-              if (on0) r.o[n][u] += w0 * x;
-              if (on1) r.o[n][2 + u] += w1 * x;
-            }
-          }
-        }
-      }
+    for (int e = 0; e < 4; ++e) {
+      w[e][0] = vr[t][e].x, w[e][1] = vr[t][e].y;
+      w[e][2] = vr[t][e].z, w[e][3] = vr[t][e].w;
     }
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      // the weights are rounded to bf16 for the tensor cores; their sum is not
-      const uint32_t p[4] = {pack_bf16x2(s[2 * t][0], s[2 * t][1]), pack_bf16x2(s[2 * t][2], s[2 * t][3]),
-                             pack_bf16x2(s[2 * t + 1][0], s[2 * t + 1][1]),
-                             pack_bf16x2(s[2 * t + 1][2], s[2 * t + 1][3])};
-      uint32_t w[4][4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        w[e][0] = vr[t][e].x, w[e][1] = vr[t][e].y;
-        w[e][2] = vr[t][e].z, w[e][3] = vr[t][e].w;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-        mma_bf16(r.o[j], p, __byte_perm(w[0][j >> 1], w[1][j >> 1], sel),
-                 __byte_perm(w[2][j >> 1], w[3][j >> 1], sel));
-      }
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+      mma_bf16(r.o[j], p, __byte_perm(w[0][j >> 1], w[1][j >> 1], sel), __byte_perm(w[2][j >> 1], w[3][j >> 1], sel));
+    }
+  }
+}
+
+// Steps of kFewStep keys, from `at` on every `stride` keys of the union.  (With SAFE in halves, which
+// leave its further registers room.)
+template <bool SAFE>
+__device__ __forceinline__ void attend_steps(Rows16& r, const KeyUnion& keys, const uint4* kp, const uint4* vp,
+                                             float scale_log2, int at, int stride) {
+#pragma unroll 1
+  for (; at < keys.count; at += stride) {
+    if constexpr (SAFE) {
+#pragma unroll 1
+      for (int half = 0; half < kFewStep; half += 16) attend_step<2, true>(r, keys, kp, vp, scale_log2, at + half);
+    } else {
+      attend_step<kFewStep / 8, false>(r, keys, kp, vp, scale_log2, at);
     }
   }
 }
@@ -426,19 +456,19 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, int sm
   const int64_t keys = most_keys(a, spans, B);
   // A tile is shared by as many CTAs as have a step for each of four warps, as long as all
   // CTAs run at once (three to an SM) or each warp has 16 steps to make up for their start and
-  // join.  1028 keys, us for 8 / 4 / 2 / 1 CTAs: 32 tiles 6.4 / 7.1 / 9.6 / 14, 96 tiles 14.8 /
-  // 10.8 / 11.8 / 15, 512 tiles 63 / 46 / 37 / 32.
+  // join.  1028 keys, us for 8 / 4 / 2 / 1 CTAs: 32 tiles 5.3 / 6.0 / 8.0 / 12, 96 tiles 12.9 /
+  // 9.5 / 9.9 / 13, 512 tiles 56 / 40 / 32 / 28.
   const int64_t tiles = (int64_t)((rows + 15) / 16) * a.kv_heads * B;
   int splits = 1;
   while (splits < kFewMaxSplit && splits * 4 * kFewStep < keys &&
          (tiles * splits * 2 <= 3 * sms || keys >= (int64_t)splits * 2 * 4 * kFewStep * 16))
     splits *= 2;
-  // past two steps a warp: eight warps a CTA (8192 keys, 32 heads on 8: 10.2 us for 15.5;
-  // 1028 keys: 15.5 for 8.0, fewer CTAs fit an SM)
+  // past two steps a warp: eight warps a CTA (8192 keys, 32 heads on 8: 8.5 us for
+  // 11.1; 1028 keys, 96 tiles: 17.6 for 13.0, fewer CTAs fit an SM)
   const bool wide = splits == kFewMaxSplit && keys > 2 * kFewMaxSplit * 4 * kFewStep;
   // and sixteen CTAs where so few tiles leave SMs idle, or the keys are many more (one query, us
-  // for sixteen / eight CTAs: 4 tiles, 2100 keys 5.4 / 6.3, 8192 keys 7.3 / 10.5, 131072 keys 69
-  // / 131; 8 tiles, 2100 keys 6.9 / 6.3, 8192 keys 9.6 / 10.6, 131072 keys 90 / 132)
+  // for sixteen / eight CTAs: 4 tiles, 2100 keys 4.6 / 5.3, 8192 keys 6.1 / 8.4, 131072 keys 59
+  // / 112; 8 tiles, 2100 keys 6.0 / 5.5, 8192 keys 8.4 / 8.5, 131072 keys 78 / 115)
   if (wide && (2 * kFewLongSplit * tiles <= sms || (kFewLongSplit * tiles <= sms && keys > 4096)) &&
       tiles <= long_clusters())
     splits = kFewLongSplit;
@@ -468,7 +498,7 @@ cudaError_t launch_few(const WindowArgs& a, const RowSpans& spans, int B, int sm
 // The rows `redo` of the sixteen from t0 on of one head, from their keys alone, by one warp.  (A
 // call, so that the many-row kernel's own registers are not spilled for it: 1 % there.)  With an
 // infinity that every row attends, 8356 tokens, window 1024 + 1024, 256 sinks and 24 heads take
-// 1.9 ms for 0.19; one row and one key at a time took 61.
+// 1.9 ms for 0.19, with nothing but NaN in V 3.6; one row and one key at a time took 61.
 __device__ __noinline__ void redo_rows(const WindowArgs& a, int b, int h, int bhk, int t0, int start, int len,
                                        uint32_t redo) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, last = min(t0 + 15, a.n_q - 1);
@@ -1015,9 +1045,9 @@ cudaError_t launch_many(const WindowArgs& a, const RowSpans& spans, int B, int* 
 // Rows are few where 16-row tiles are hardly more than 128-row ones (per key head; both
 // read the same keys), or up to three times as many but so few in all that their keys can be
 // split.  Over 1028 of 4352 keys, us for 16-row tiles (128-row tiles): 24 heads on as many key
-// heads, 1 query 6.2 (14.0), 32 queries 8.4 (15.9), 48 queries 10.9 (14.6), 4 sequences of 48
-// 21.6 (16.8); 24 heads on 8 key heads, 48 queries 10.8 (14.7), 4 sequences of 16 10.8 (16.2),
-// of 32 17.0 (15.1), 16 of 32 43 (35).
+// heads, 1 query 5.1 (12.8), 32 queries 7.4 (14.6), 48 queries 9.1 (14.6), 4 sequences of 48
+// 19.0 (15.5); 24 heads on 8 key heads, 48 queries 9.0 (14.6), 4 sequences of 16 9.6 (14.8),
+// of 32 14.1 (14.9), 16 of 32 38 (33).
 bool few_rows(const WindowArgs& a, int B, int sms) {
   const int64_t group = a.heads / a.kv_heads;
   const int64_t small = (a.n_q * group + 15) / 16, large = group * ((a.n_q + tc::BQ - 1) / tc::BQ);
