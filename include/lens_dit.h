@@ -431,18 +431,26 @@ LENS_API lens_status lens_op_sandwich_norm(const float* h, const void* y, lens_d
  * a window of `left` keys before and `right` keys after its own position, and the first
  * `sinks` keys wherever the window is (right = 0 is causal, sinks included).  Over joint
  * [text; image] tokens with sinks = n_txt every image token sees the whole text.
- *   out = softmax(scale * q k^T) v over the attended keys, zeros where there are none.
+ *   out = softmax(scale * q k^T) v over the attended keys, zeros where there are none (or where
+ * every score is -inf).  Scores, their maxima and the sums of the weights are fp32.  The weights
+ * exp(score - m) are rounded to bf16 for the product with v, where m is the row's running maximum
+ * or (for many queries) up to 8 ln 2 below it; their sum is not rounded.  So an output may be off
+ * by 2^-8 of sum_j p_j |v_j| besides its own rounding.
  *   q dev bf16 [B, heads, n_q, 64];  k, v dev bf16 [B, kv_heads, n_kv, 64], query head h
  *   reads key head h / (heads / kv_heads);  out dev bf16 [B, n_q, heads * 64]
- *   q_start  host int [B], >= 0, or NULL (0);  kv_len host int [B], 0..n_kv, or NULL (n_kv)
+ *   q_start  host int [B], >= 0, or NULL (0);  kv_len host int [B], 0..n_kv, or NULL (n_kv).
+ *            They are read during the call: a captured call keeps them, so a graph replays with the
+ *            lengths it was captured with.
  *   left, right  >= 0, or -1 for no bound on that side;  sinks >= 0
  * Keys that a query does not attend have no effect on its output, whatever K and V hold
  * there.  Rows of a tile that reads an infinity or NaN in V are computed a second time, which may
- * round differently; where every row attends one, a call takes up to ten times as long.  n_q may be
- * anything from one token against a long cache to all of them.  (For few queries, up to about 48, the keys are
- * split over more CTAs in a small batch than in a large one, so the last bit of a row may
- * depend on the batch; for more queries it does not.)  B <= 64; heads a multiple of kv_heads, at
- * most 1024; q, k, v, out 16-byte aligned; out must not overlap q, k or v.
+ * round differently; where every row attends one, a call takes up to ten times as long, and up to
+ * twenty times where V holds little else.
+ * n_q may be anything from one token against a long cache to all of them.  (For few queries, up to
+ * about 48, the keys are split over more CTAs in a small batch or one with a long sequence, so a row
+ * may differ from batch to batch within the bound above; for more queries it does not.)
+ * B <= 64; heads a multiple of kv_heads, at most 1024; q, k, v, out 16-byte aligned; out must not
+ * overlap q, k or v.
  * Errors: INVALID_ARG (NULL, misaligned, scale <= 0 or not finite times log2(e), left or
  * right < -1, sinks < 0), SHAPE (B, heads, kv_heads, n_q, n_kv < 1, lengths or starts out of range,
  * q_start + n_q or n_kv > 2^29). */
